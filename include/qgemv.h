@@ -43,8 +43,9 @@
  *    and no output was touched.  QG_ERR_LAUNCH reports a failed launch of
  *    the call's own kernels (an error that an earlier, unrelated HIP call
  *    left for the calling thread is cleared before the first launch).
- *  - Data errors that only the device can see (expert ids) are reported in a
- *    caller-provided device int32 status word (see moe_routed_qgemv).
+ *  - Data errors that only the device can see (expert ids, lengths, page ids)
+ *    are reported in a caller-provided device int32 status word (see
+ *    moe_routed_qgemv and the attention section).
  *  - The library's only process-wide state is set-up done once per device
  *    (the device's compute-unit count, kernels' dynamic-LDS limits), kept per
  *    device behind one lock, so calls from several host threads, on several
@@ -116,6 +117,14 @@ extern "C" {
 #define QG_DEV_OK 0
 #define QG_DEV_BAD_EXPERT 1  /* an expert id outside [0, E) */
 #define QG_DEV_NULL_EXPERT 2 /* a selected expert has a NULL or misaligned weight pointer */
+/* device status word values (the key/value cache and attention calls) */
+#define QG_DEV_BAD_LENGTH 3 /* a sequence length or offset that its call rules out */
+#define QG_DEV_BAD_PAGE 4   /* a page id outside [0, num_pages) */
+
+/* element types of keys, values and queries */
+#define QG_TYPE_F32 0
+#define QG_TYPE_F16 1
+#define QG_TYPE_BF16 2
 
 /* weight formats */
 #define QG_FMT_Q8_0 0
@@ -129,6 +138,11 @@ extern "C" {
 #define QG_MAX_PREFILL_M 65536 /* largest token count of qgemm_q8_0 */
 #define QG_MAX_MOE_PAIRS 8192 /* largest T * topk of moe_routed_qgemv */
 #define QG_MAX_EXPERTS 4096   /* largest E of moe_routed_qgemv */
+#define QG_MAX_SEQS 65535       /* largest B of the cache and attention calls */
+#define QG_MAX_HEADS 1024       /* largest H and Hkv */
+#define QG_MAX_PAGE 65536       /* largest page, in positions */
+#define QG_MAX_DECODE_TOKENS 16 /* largest Tq of attn_decode_kv4 */
+#define QG_MAX_ATTN_TOKENS (1 << 24) /* most packed tokens of one call */
 
 /* ---- activation quantization ------------------------------------------- */
 /*
@@ -438,6 +452,141 @@ size_t qgemm_prefill_workspace_bytes(int M, int K);
  */
 int qgemm_prefill_ws(int fmt, const void *W, int N, int K, const uint16_t *x_bf16, int M, float *y, void *ws,
                      size_t ws_bytes, void *stream);
+
+/* ---- attention --------------------------------------------------------- */
+/*
+ * Attention between the query/key/value projections and the (grouped)
+ * attention-output projection of a decode step or a prompt.  H query heads
+ * share Hkv key/value heads (H % Hkv == 0; query head h reads key/value head
+ * h / (H / Hkv)), heads are Dh = 64, 128 or 256 wide.  One sequence has `len`
+ * positions, 0 .. len-1; the query at position p sees the keys j <= p, and with
+ * window > 0 only those with j > p - window (window = 0: all).  For each query
+ *   y = sum_j softmax_j(scale * q . k_j) v_j     over the keys it sees,
+ * and y = 0 where it sees none.  scale is any finite number.
+ *
+ * q, k and v are rows of packed heads, [tokens, heads, Dh], whose rows may be
+ * further apart than heads * Dh: ldq, ldk, ldv count elements from one token
+ * to the next, so that each may be a part of one fused projection's output
+ * (every row 16-byte aligned: base pointers and row strides in bytes are
+ * multiples of 16).  Outputs named y are dense.  int32 arrays need 4-byte
+ * alignment.  Every sequence's own keys and values must be finite; what lies
+ * elsewhere (rows of other sequences, positions behind a sequence, unused pages) may
+ * hold anything and has no influence.
+ *
+ * The cache.  Keys and values are held in pages of `page` positions (a power
+ * of two, 16 .. QG_MAX_PAGE) of one sequence: `kv` is num_pages pages of
+ * kv4_page_bytes(page, Hkv, Dh) bytes, pages int32 [B, max_pages] names the
+ * page of each block of positions, lens int32 [B] the positions of each
+ * sequence.  Entries of `pages` behind a sequence's last position are not
+ * read.  Sequences may share pages that are only read.  Inside a page, head
+ * after head, one head's region is (P = page, 4-bit codes as in
+ * QG_FMT_FP4_E2M1_MX, one UE8M0 scale for 32 channels of one position):
+ *   key codes    uint8 [P][Dh/2]         byte i: channels 2i (low nibble), 2i+1
+ *   value codes  uint8 [P/4][Dh/8][4][4] channel c of position t in byte
+ *                                        ((t/4 * Dh/8 + c/8) * 4 + t%4) * 4 + c%8/2
+ *   key scales   uint8 [P][Dh/32]
+ *   value scales uint8 [P/4][Dh/32][4]   position t innermost
+ *
+ * Data errors: the calls check lengths, offsets and page ids on the device and
+ * set *d_status to QG_DEV_BAD_LENGTH or QG_DEV_BAD_PAGE (the larger one, if
+ * both occur); a call that finds none leaves *d_status as it was, so the
+ * caller sets it to QG_DEV_OK before its first call and may check it after
+ * several.  What an error leaves out is said at each call; everything else is
+ * computed, and no access leaves the arrays.
+ */
+
+/*
+ * kv4_page_bytes -- bytes of one page: Hkv * page * Dh * 17/16 (0 if a size is
+ * out of range).
+ */
+size_t kv4_page_bytes(int page, int Hkv, int Dh);
+
+/*
+ * kv4_append -- new tokens' keys and values into the cache (the FP4 elements,
+ * blocks and scales of [ATOMQ]).  k, v [n, Hkv, Dh] of QG_TYPE_* type are the packed
+ * new tokens of B sequences: sequence b's are tokens cu[b] .. cu[b+1]-1 (cu
+ * int32 [B+1], may repeat), and they become its last positions: token
+ * cu[b+1]-1 goes to position lens[b]-1 (lens counts them already).  Tokens
+ * before cu[0] and from cu[B] on are ignored.
+ * For each 32 channels x of a token and head:
+ *   e = least integer >= -120 with max |x| <= 6 * 2^e;  scale byte = e + 127;
+ *   code = the E2M1 value nearest to |x| * 2^-e, the even code on a tie, with
+ *   the sign bit of x.
+ * Every step is exact, so the bytes are determined.  NaN or Inf are outside the
+ * contract.  Two new tokens that name the same place (a page that two sequences
+ * of the call share) leave either one's bytes or a mix.
+ * Data errors: sequence b is left out if cu[b] < 0, cu[b+1] < cu[b], cu[b+1] > n,
+ * lens[b] < its new tokens or lens[b] > max_pages * page (where cu decreases, any other
+ * sequence may be left out too); a bad page's positions are left out.
+ * Errors: QG_ERR_FORMAT (type); QG_ERR_NULL; QG_ERR_SHAPE unless 1 <= n <=
+ * QG_MAX_ATTN_TOKENS, 1 <= B <= QG_MAX_SEQS, 1 <= Hkv <= QG_MAX_HEADS, Dh and page
+ * as above, max_pages >= 1, max_pages * page < 2^30, num_pages >= 1, ldk, ldv >= Hkv * Dh with
+ * 16-byte rows; QG_ERR_ALIGN; QG_ERR_LAUNCH.
+ */
+int kv4_append(int type, const void *k, int ldk, const void *v, int ldv, int n, const int32_t *cu,
+               const int32_t *lens, int B, int Hkv, int Dh, const int32_t *pages, int max_pages, int page,
+               int num_pages, void *kv, int32_t *d_status, void *stream);
+
+/*
+ * kv4_gather -- the inverse: the last cu[b+1]-cu[b] cached positions of each
+ * sequence as rows cu[b] .. cu[b+1]-1 of k and v (all of them where that is
+ * lens[b]), as a later chunk of a prompt needs them (attn_prefill).  Exact for
+ * QG_TYPE_F32 and QG_TYPE_BF16; QG_TYPE_F16 rounds (scales below 2^-23) and
+ * overflows (values above 65504) as the type does.  Rows that belong to no sequence, or to
+ * one left out by a data error, and parts of rows between Hkv * Dh and ldk or ldv are not written.
+ * Data errors and errors: as kv4_append.
+ */
+int kv4_gather(int type, void *k, int ldk, void *v, int ldv, int n, const int32_t *cu, const int32_t *lens, int B,
+               int Hkv, int Dh, const int32_t *pages, int max_pages, int page, int num_pages, const void *kv,
+               int32_t *d_status, void *stream);
+
+/*
+ * attn_decode_kv4 -- attention of the last Tq tokens of each sequence over the
+ * cache that holds them already: one token a step, or the few that are
+ * verified together ([PR623] commits list).  q [B * Tq, H, Dh] of QG_TYPE_* type, token t
+ * of sequence b in row b * Tq + t, at position lens[b] - Tq + t; y fp32
+ * [B * Tq, H * Dh], what quantize_act_q8 takes.  A query at a negative position
+ * (lens[b] < Tq) sees nothing.  max_len: a bound on lens that the host knows
+ * (the work is laid out for it), at most max_pages * page.
+ * q enters as it is and the codes are exact; scores, softmax and sums are fp32, with
+ * the weights of the values carried to 16 bits or more: the error is that of
+ * fp32 arithmetic (about 1e-6 of the norm).  A sequence's result does not depend on the others.
+ * ws: attn_decode_workspace_bytes(B, Tq, H, Hkv, Dh, max_len, window) bytes of
+ * device memory, contents ignored and left unspecified; calls that share it
+ * must be ordered on one stream.
+ * Data errors: lens[b] outside [0, max_len] gives y = 0 for sequence b; the
+ * positions of a bad page are left out, as if no query saw them.
+ * Errors: QG_ERR_FORMAT (type); QG_ERR_NULL; QG_ERR_SHAPE unless 1 <= Tq <=
+ * QG_MAX_DECODE_TOKENS, 1 <= H <= QG_MAX_HEADS, H % Hkv == 0, window >= 0, 1 <= max_len <=
+ * max_pages * page, scale finite, ldq >= H * Dh with 16-byte rows, and as kv4_append;
+ * QG_ERR_ALIGN; QG_ERR_WORKSPACE; QG_ERR_LAUNCH.
+ */
+size_t attn_decode_workspace_bytes(int B, int Tq, int H, int Hkv, int Dh, int max_len, int window);
+int attn_decode_kv4(int type, const void *q, int ldq, const int32_t *lens, int B, int Tq, int H, int Hkv, int Dh,
+                    float scale, int window, int max_len, const int32_t *pages, int max_pages, int page,
+                    int num_pages, const void *kv, float *y, void *ws, size_t ws_bytes, int32_t *d_status,
+                    void *stream);
+
+/*
+ * attn_prefill -- causal attention of packed prompts on the matrix cores.
+ * q [nq, H, Dh], k, v [nk, Hkv, Dh] and y [nq, H * Dh] of one 16-bit type
+ * (QG_TYPE_F16, QG_TYPE_BF16).  Sequence b has queries cu_q[b] .. cu_q[b+1]-1 and
+ * keys cu_k[b] .. cu_k[b+1]-1 (int32 [B+1] each, may repeat); with Lq queries and Lk keys, query i
+ * stands at position Lk - Lq + i: a whole prompt has Lq = Lk, a later chunk
+ * fewer queries than keys.  Queries at negative positions see nothing.
+ * Scores, softmax and sums are fp32; the weights are rounded to the type for
+ * their product with v, and y once at the end.  Rows of y that belong to no
+ * sequence are not written.
+ * Data errors: a sequence with cu[b] < 0, cu[b+1] < cu[b] or cu[b+1] > its token count in
+ * either array is left out (its y is not written); where offsets decrease,
+ * any other sequence may be left out too.
+ * Errors: QG_ERR_FORMAT (type); QG_ERR_NULL; QG_ERR_SHAPE unless 1 <= nq, nk <=
+ * QG_MAX_ATTN_TOKENS, 1 <= B <= QG_MAX_SEQS, 1 <= H <= QG_MAX_HEADS, H % Hkv == 0, Dh
+ * as above, window >= 0, scale finite, row strides as above; QG_ERR_ALIGN; QG_ERR_LAUNCH.
+ */
+int attn_prefill(int type, const void *q, int ldq, const void *k, int ldk, const void *v, int ldv, int nq, int nk,
+                 const int32_t *cu_q, const int32_t *cu_k, int B, int H, int Hkv, int Dh, float scale, int window,
+                 void *y, int32_t *d_status, void *stream);
 
 /* ---- diagnostics ------------------------------------------------------- */
 /* Human-readable text for a QG_* status or QG_DEV_* value (static storage). */

@@ -21,14 +21,16 @@ __all__ = [
     "qgemv_q8_0_f32", "qgemv_q4k_f32", "qgemv_paired_f32", "qgemm_prefill_workspace_bytes", "qgemm_prefill_ws",
     "qgemv_grouped", "qgemv_q8_0_quality", "FMT_FP8_E4M3_B128", "FMT_FP4_E2M1_MX", "qg_matrix_bytes", "qgemv_mx",
     "moe_routed_qgemv_fmt", "qgemm_q8_0", "qg_stream_read_bursts", "qg_stream_read", "moe_routed_qgemv_noalloc",
-    "MOE_SCRATCH_BYTES",
+    "MOE_SCRATCH_BYTES", "TYPE_F32", "TYPE_F16", "TYPE_BF16", "kv4_page_bytes", "kv4_append", "kv4_gather",
+    "attn_decode_workspace_bytes", "attn_decode_kv4", "attn_prefill",
 ]
 
 FMT_Q8_0 = 0
 FMT_Q4K = 1
 FMT_FP8_E4M3_B128 = 2
 FMT_FP4_E2M1_MX = 3
-DEV_OK, DEV_BAD_EXPERT, DEV_NULL_EXPERT = 0, 1, 2
+DEV_OK, DEV_BAD_EXPERT, DEV_NULL_EXPERT, DEV_BAD_LENGTH, DEV_BAD_PAGE = 0, 1, 2, 3, 4
+TYPE_F32, TYPE_F16, TYPE_BF16 = 0, 1, 2  # QG_TYPE_*
 MAX_K, MAX_M, MAX_MOE_PAIRS, MAX_EXPERTS = 16384, 32, 8192, 4096
 WS_REGIONS = ["NUNIQ", "UNIQ", "SLOT", "PAIR_OFF", "PAIRS", "G", "V", "H", "HQ", "HD", "HS", "O", "HOT"]
 MOE_MM_PAIRS = 9  # QG_MOE_MM_PAIRS
@@ -91,6 +93,16 @@ _c_read_bursts = _sig("qg_stream_read_bursts", _sz, [_sz, _i])
 _c_read = _sig("qg_stream_read", _i, [_vp, _sz, _i, _i, _vp, _sz, _vp])
 _c_moe_noalloc = _sig("moe_routed_qgemv_noalloc", _i, [_i, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp,
                                                       _vp, _vp, _vp, _vp])
+_cache_sig = [_vp, _i, _i, _i, _vp]  # pages, max_pages, page, num_pages, kv
+_c_kv4_bytes = _sig("kv4_page_bytes", _sz, [_i, _i, _i])
+_kv4_sig = [_i, _vp, _i, _vp, _i, _i, _vp, _vp, _i, _i, _i, *_cache_sig, _vp, _vp]
+_c_kv4_append = _sig("kv4_append", _i, _kv4_sig)
+_c_kv4_gather = _sig("kv4_gather", _i, _kv4_sig)
+_c_decode_ws = _sig("attn_decode_workspace_bytes", _sz, [_i] * 7)
+_c_decode = _sig("attn_decode_kv4", _i, [_i, _vp, _i, _vp, _i, _i, _i, _i, _i, ctypes.c_float, _i, _i, *_cache_sig,
+                                         _vp, _vp, _sz, _vp, _vp])
+_c_attn_prefill = _sig("attn_prefill", _i, [_i, _vp, _i, _vp, _i, _vp, _i, _i, _i, _vp, _vp, _i, _i, _i, _i,
+                                            ctypes.c_float, _i, _vp, _vp, _vp])
 
 
 class QGError(RuntimeError):
@@ -245,3 +257,109 @@ def moe_routed_qgemv_noalloc(fmt: int, qx, dx, sx, T: int, D: int, F: int, E: in
                              down, y, d_status, stream=None) -> None:
     _ok(_c_moe_noalloc(fmt, _ptr(qx), _ptr(dx), _ptr(sx), T, D, F, E, topk, _ptr(ids), _ptr(rw), _ptr(gate),
                        _ptr(up), _ptr(down), _ptr(y), _ptr(d_status), _stream(stream, qx)), "moe_routed_qgemv_noalloc")
+
+
+# The attention calls take rows that may be further apart than they are wide
+# (parts of a fused projection), so they check each tensor against the sizes
+# that the kernels will use.
+_TYPE_NAMES = {TYPE_F32: "torch.float32", TYPE_F16: "torch.float16", TYPE_BF16: "torch.bfloat16"}
+
+
+def _rows_ptr(t, name: str, type: int, rows: int, width: int, ld: int):
+    """Device pointer of `rows` rows of `width` elements, `ld` elements apart."""
+    if t is None or not hasattr(t, "data_ptr"):
+        return _ptr(t)
+    if not t.is_cuda:
+        raise TypeError("libqgemv takes device tensors; got %s on %s" % (name, t.device))
+    if type in _TYPE_NAMES and str(t.dtype) != _TYPE_NAMES[type]:
+        raise TypeError("%s is %s, the call's type is %s" % (name, t.dtype, _TYPE_NAMES[type]))
+    n = t.shape[0] if t.dim() else 0
+    dense = t.is_contiguous() or (n > 0 and t[0].is_contiguous())
+    each = t.numel() // n if n else 0
+    if t.is_contiguous() and each != width:  # a flat or differently folded tensor
+        have, step = t.numel(), ld
+        fits = have >= (rows - 1) * ld + width
+    else:
+        step = t.stride(0) if n > 1 else ld
+        fits = dense and each == width and n >= rows
+    if not fits or step != ld:
+        raise ValueError("%s: %d rows of %d elements, %d apart, do not lie in a tensor of shape %s and strides %s" % (
+            name, rows, width, ld, tuple(t.shape), tuple(t.stride())))
+    return t.data_ptr()
+
+
+def _array_ptr(t, name: str, dtype: str, count: int):
+    """Device pointer of a dense tensor that holds `count` values of dtype (None: any type, counted in bytes)."""
+    if t is None or not hasattr(t, "data_ptr"):
+        return _ptr(t)
+    have = t.numel() if dtype else t.numel() * t.element_size()
+    if dtype and str(t.dtype) != "torch." + dtype:
+        raise TypeError("%s is %s, not torch.%s" % (name, t.dtype, dtype))
+    if have < count:
+        raise ValueError("%s holds %d, the call needs %d" % (name, have, count))
+    return _ptr(t)
+
+
+def _call_on(what: str, f, first, args, stream):
+    """f(*args, stream) with the device of tensor `first` current, as its launch needs."""
+    if hasattr(first, "device"):
+        import torch
+        if first.device.index != torch.cuda.current_device():
+            with torch.cuda.device(first.device):
+                _ok(f(*args, _stream(stream, first)), what)
+            return
+    _ok(f(*args, _stream(stream, first)), what)
+
+
+def _cache_args(pages, B: int, max_pages: int, page: int, num_pages: int, Hkv: int, Dh: int, kv):
+    return (_array_ptr(pages, "pages", "int32", B * max_pages), max_pages, page, num_pages,
+            _array_ptr(kv, "kv", None, num_pages * kv4_page_bytes(page, Hkv, Dh)))
+
+
+def kv4_page_bytes(page: int, Hkv: int, Dh: int) -> int:
+    return int(_c_kv4_bytes(page, Hkv, Dh))
+
+
+def _kv4(what, f, type, k, ldk, v, ldv, n, cu, lens, B, Hkv, Dh, pages, max_pages, page, num_pages, kv, d_status,
+         stream):
+    w = Hkv * Dh
+    _call_on(what, f, k, (type, _rows_ptr(k, "k", type, n, w, ldk), ldk, _rows_ptr(v, "v", type, n, w, ldv), ldv, n,
+                          _array_ptr(cu, "cu", "int32", B + 1), _array_ptr(lens, "lens", "int32", B), B, Hkv, Dh,
+                          *_cache_args(pages, B, max_pages, page, num_pages, Hkv, Dh, kv),
+                          _array_ptr(d_status, "d_status", "int32", 1)), stream)
+
+
+def kv4_append(type: int, k, ldk: int, v, ldv: int, n: int, cu, lens, B: int, Hkv: int, Dh: int, pages,
+               max_pages: int, page: int, num_pages: int, kv, d_status, stream=None) -> None:
+    _kv4("kv4_append", _c_kv4_append, type, k, ldk, v, ldv, n, cu, lens, B, Hkv, Dh, pages, max_pages, page,
+         num_pages, kv, d_status, stream)
+
+
+def kv4_gather(type: int, k, ldk: int, v, ldv: int, n: int, cu, lens, B: int, Hkv: int, Dh: int, pages,
+               max_pages: int, page: int, num_pages: int, kv, d_status, stream=None) -> None:
+    _kv4("kv4_gather", _c_kv4_gather, type, k, ldk, v, ldv, n, cu, lens, B, Hkv, Dh, pages, max_pages, page,
+         num_pages, kv, d_status, stream)
+
+
+def attn_decode_workspace_bytes(B: int, Tq: int, H: int, Hkv: int, Dh: int, max_len: int, window: int) -> int:
+    return int(_c_decode_ws(B, Tq, H, Hkv, Dh, max_len, window))
+
+
+def attn_decode_kv4(type: int, q, ldq: int, lens, B: int, Tq: int, H: int, Hkv: int, Dh: int, scale: float,
+                    window: int, max_len: int, pages, max_pages: int, page: int, num_pages: int, kv, y, ws,
+                    ws_bytes: int, d_status, stream=None) -> None:
+    _call_on("attn_decode_kv4", _c_decode, q,
+             (type, _rows_ptr(q, "q", type, B * Tq, H * Dh, ldq), ldq, _array_ptr(lens, "lens", "int32", B), B, Tq, H,
+              Hkv, Dh, scale, window, max_len, *_cache_args(pages, B, max_pages, page, num_pages, Hkv, Dh, kv),
+              _array_ptr(y, "y", "float32", B * Tq * H * Dh), _array_ptr(ws, "ws", None, ws_bytes), ws_bytes,
+              _array_ptr(d_status, "d_status", "int32", 1)), stream)
+
+
+def attn_prefill(type: int, q, ldq: int, k, ldk: int, v, ldv: int, nq: int, nk: int, cu_q, cu_k, B: int, H: int,
+                 Hkv: int, Dh: int, scale: float, window: int, y, d_status, stream=None) -> None:
+    w = Hkv * Dh
+    _call_on("attn_prefill", _c_attn_prefill, q,
+             (type, _rows_ptr(q, "q", type, nq, H * Dh, ldq), ldq, _rows_ptr(k, "k", type, nk, w, ldk), ldk,
+              _rows_ptr(v, "v", type, nk, w, ldv), ldv, nq, nk, _array_ptr(cu_q, "cu_q", "int32", B + 1),
+              _array_ptr(cu_k, "cu_k", "int32", B + 1), B, H, Hkv, Dh, scale, window,
+              _rows_ptr(y, "y", type, nq, H * Dh, H * Dh), _array_ptr(d_status, "d_status", "int32", 1)), stream)

@@ -14,6 +14,8 @@ extern "C" const char *qg_status_string(int status) {
         case QG_ERR_FORMAT: return "unknown weight format";
         case QG_ERR_WORKSPACE: return "workspace too small";
         case QG_ERR_LAUNCH: return "kernel launch failed";
+        case QG_DEV_BAD_LENGTH: return "a sequence length or offset is out of range";
+        case QG_DEV_BAD_PAGE: return "a page id is outside the cache";
         default: break;
     }
     return "unknown status";
