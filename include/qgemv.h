@@ -462,7 +462,7 @@ int qgemm_prefill_ws(int fmt, const void *W, int N, int K, const uint16_t *x_bf1
  * positions, 0 .. len-1; the query at position p sees the keys j <= p, and with
  * window > 0 only those with j > p - window (window = 0: all).  For each query
  *   y = sum_j softmax_j(scale * q . k_j) v_j     over the keys it sees,
- * and y = 0 where it sees none.  scale is any finite number.
+ * and y = 0 where it sees none.  |scale| < 2^127.
  *
  * q, k and v are rows of packed heads, [tokens, heads, Dh], whose rows may be
  * further apart than heads * Dh: ldq, ldk, ldv count elements from one token
@@ -558,7 +558,7 @@ int kv4_gather(int type, void *k, int ldk, void *v, int ldv, int n, const int32_
  * positions of a bad page are left out, as if no query saw them.
  * Errors: QG_ERR_FORMAT (type); QG_ERR_NULL; QG_ERR_SHAPE unless 1 <= Tq <=
  * QG_MAX_DECODE_TOKENS, 1 <= H <= QG_MAX_HEADS, H % Hkv == 0, window >= 0, 1 <= max_len <=
- * max_pages * page, scale finite, ldq >= H * Dh with 16-byte rows, and as kv4_append;
+ * max_pages * page, |scale| < 2^127, ldq >= H * Dh with 16-byte rows, and as kv4_append;
  * QG_ERR_ALIGN; QG_ERR_WORKSPACE; QG_ERR_LAUNCH.
  */
 size_t attn_decode_workspace_bytes(int B, int Tq, int H, int Hkv, int Dh, int max_len, int window);
@@ -582,7 +582,7 @@ int attn_decode_kv4(int type, const void *q, int ldq, const int32_t *lens, int B
  * any other sequence may be left out too.
  * Errors: QG_ERR_FORMAT (type); QG_ERR_NULL; QG_ERR_SHAPE unless 1 <= nq, nk <=
  * QG_MAX_ATTN_TOKENS, 1 <= B <= QG_MAX_SEQS, 1 <= H <= QG_MAX_HEADS, H % Hkv == 0, Dh
- * as above, window >= 0, scale finite, row strides as above; QG_ERR_ALIGN; QG_ERR_LAUNCH.
+ * as above, window >= 0, |scale| < 2^127, row strides as above; QG_ERR_ALIGN; QG_ERR_LAUNCH.
  */
 int attn_prefill(int type, const void *q, int ldq, const void *k, int ldk, const void *v, int ldv, int nq, int nk,
                  const int32_t *cu_q, const int32_t *cu_k, int B, int H, int Hkv, int Dh, float scale, int window,

@@ -79,7 +79,7 @@ extern "C" int attn_prefill(int type, const void *q, int ldq, const void *k, int
     if (!q || !k || !v || !cu_q || !cu_k || !y || !d_status) return QG_ERR_NULL;
     if (B < 1 || B > QG_MAX_SEQS || H < 1 || H > QG_MAX_HEADS || Hkv < 1 || H % Hkv != 0 ||
         (Dh != 64 && Dh != 128 && Dh != 256) || nq < 1 || nq > QG_MAX_ATTN_TOKENS || nk < 1 ||
-        nk > QG_MAX_ATTN_TOKENS || window < 0 || !__builtin_isfinite(scale))
+        nk > QG_MAX_ATTN_TOKENS || window < 0 || !__builtin_isfinite(2.f * scale))
         return QG_ERR_SHAPE;
     if (!row_stride_ok(type, ldq, H * Dh) || !row_stride_ok(type, ldk, Hkv * Dh) || !row_stride_ok(type, ldv, Hkv * Dh))
         return QG_ERR_SHAPE;
