@@ -1,9 +1,27 @@
-// Causal attention of packed prompts.  The simple form: one wave per query row
-// and head, 64 keys at a time, fp32 throughout.
+// Causal attention of packed prompts on the matrix cores.
+//
+// One pass over the keys with the running maximum and sum of a softmax.  A
+// workgroup takes 128 queries of one head, 32 a wave, and walks its keys in
+// tiles that it copies into two LDS stages, the next tile's copy in flight
+// while the current one is used:
+//   S^T = K Q^T    (keys x queries),  O^T += V^T P^T   (channels x queries),
+// both as v_mfma_f32_32x32x16.  With the products transposed a lane keeps one
+// query throughout, and the scores that it receives are the weights that it
+// has to supply: P never leaves the registers.  K is read from LDS by rows, V
+// by columns (the transposing LDS read); 16-byte pieces of a row are stored
+// permuted by the row's number so that neither read meets a bank twice.
+// Weights are rounded to the 16-bit type for their product with V, as is
+// y: the two roundings are of one size, and scores, maxima and sums are fp32.
+#include <type_traits>
+
 #include "common.h"
 #include "kv4_device.h"
 
 namespace qg {
+
+constexpr int kPreWaves = 4;
+constexpr int kPreRows = 32 * kPreWaves;  // queries of a workgroup
+constexpr float kPreSlack = 8.f;          // a weight may reach 2^8 before the sums are rescaled
 
 struct PrefillArgs {
     const void *q, *k, *v;
@@ -11,62 +29,247 @@ struct PrefillArgs {
     const int32_t *cu_q, *cu_k;
     int32_t *status;
     int ldq, ldk, ldv, nq, nk, B, H, G, window;
-    float scale;
+    float scale;  // times log2(e), not negative
+    int flip;     // queries change sign (a negative scale) or vanish (scale 0)
+    int slots;    // query tiles, over all sequences, with room to spare
 };
 
+template <int TYPE>
+struct PreElem;
+template <>
+struct PreElem<QG_TYPE_F16> {
+    typedef f16x8 x8;
+    __device__ static f32x16 mfma(u32x4 a, u32x4 b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
+                                                      0, 0);
+    }
+    __device__ static uint32_t pack(float a, float b) {
+        return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
+    }
+};
+template <>
+struct PreElem<QG_TYPE_BF16> {
+    typedef bf16x8 x8;
+    __device__ static f32x16 mfma(u32x4 a, u32x4 b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
+                                                       0, 0, 0);
+    }
+    __device__ static uint32_t pack(float a, float b) {
+        return __builtin_bit_cast(uint32_t, bf16x2{(bf16_t)a, (bf16_t)b});
+    }
+};
+
+// Keys of a tile, and where the 16-byte piece p of row r is held: reads of one
+// piece of many rows (keys) or of four pieces of four rows (values) then fall
+// into different banks.
+template <int DH>
+struct PreTile {
+    static constexpr int N = DH == 256 ? 32 : 64, CH = DH / 8, BYTES = N * DH * 2;
+    __device__ static int k_piece(int r, int p) { return p ^ (r & (CH < 16 ? CH - 1 : 15)); }
+    __device__ static int v_piece(int r, int p) { return p ^ (DH == 64 ? (r >> 1 & 1) << 2 : (r & 3) << 2); }
+};
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// Four rows of one column each, out of LDS.
+__device__ __forceinline__ u32x2 lds_read_column4(const char *p) {
+    const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) s16x4 *)const_cast<char *>(p));
+    return __builtin_bit_cast(u32x2, x);
+}
+
+__device__ __forceinline__ float half_max(float x) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, x);
+    const auto p = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return __builtin_fmaxf(__builtin_bit_cast(float, (uint32_t)p[0]), __builtin_bit_cast(float, (uint32_t)p[1]));
+}
+
+__device__ __forceinline__ bool pre_lengths_ok(const PrefillArgs &a, int q0, int q1, int k0, int k1) {
+    return q0 >= 0 && q1 >= q0 && q1 <= a.nq && k0 >= 0 && k1 >= k0 && k1 <= a.nk;
+}
+
 template <int TYPE, int DH>
-__global__ __launch_bounds__(64) void attn_prefill_simple_kernel(PrefillArgs a) {
+__global__ __launch_bounds__(kPreWaves *kWave, 2) void attn_prefill_kernel(PrefillArgs a) {
     typedef typename ElemOf<TYPE>::type T;
-    constexpr int C = DH / 64;
-    const int row = blockIdx.x, h = blockIdx.y, hk = h / a.G, lane = threadIdx.x;
-    if (row == 0 && h == 0)
-        for (int b = lane; b < a.B; b += 64)
-            if (a.cu_q[b] < 0 || a.cu_q[b + 1] < a.cu_q[b] || a.cu_q[b + 1] > a.nq || a.cu_k[b] < 0 ||
-                a.cu_k[b + 1] < a.cu_k[b] || a.cu_k[b + 1] > a.nk)
+    typedef PreElem<TYPE> E;
+    typedef PreTile<DH> L;
+    constexpr int N = L::N, NT = N / 32, KC = DH / 16, MT = DH / 32;
+    // four objects: the compiler tells the copies in flight into one from the reads of another
+    __shared__ __attribute__((aligned(16))) char sk0[L::BYTES], sk1[L::BYTES], sv0[L::BYTES], sv1[L::BYTES];
+    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int c = lane & 31, hf = lane >> 5;
+
+    // Workgroups are dealt to the 8 XCDs in turn: where the heads divide by 8,
+    // each XCD takes its own heads, so a key/value head's tiles are fetched
+    // into one L2.  The last queries of a sequence, which see most, go first.
+    const int id = blockIdx.x;
+    int h, slot;
+    if (a.H % 8 == 0) {
+        const int per = a.H / 8, i = id >> 3;
+        h = (id & 7) * per + i % per;
+        slot = a.slots - 1 - i / per;
+    } else {
+        h = id % a.H;
+        slot = a.slots - 1 - id / a.H;
+    }
+    if (id == 0)
+        for (int b = threadIdx.x; b < a.B; b += kPreWaves * kWave)
+            if (!pre_lengths_ok(a, a.cu_q[b], a.cu_q[b + 1], a.cu_k[b], a.cu_k[b + 1]))
                 kv4_report(a.status, QG_DEV_BAD_LENGTH);
-    const int b = wave_find_last(a.B, row, [&](int s) { return a.cu_q[s]; });
-    const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
-    if (q0 < 0 || q1 > a.nq || k0 < 0 || k1 < k0 || k1 > a.nk || row < q0 || row >= q1) return;
-    const int end = min(k1 - k0, row - q0 + (k1 - k0) - (q1 - q0) + 1);
-    const int begin = a.window ? max(0, end - a.window) : 0;
-    const T *q = (const T *)a.q + (size_t)row * a.ldq + h * DH;
-    float mx = -INFINITY, l = 0.f, acc[C] = {};
-    for (int j0 = begin; j0 < end; j0 += 64) {
-        const int j = j0 + lane;
-        float s = -INFINITY;
-        if (j < end) {
-            const T *k = (const T *)a.k + (size_t)(k0 + j) * a.ldk + hk * DH;
-            s = 0.f;
-            for (int i = 0; i < DH; ++i) s += (float)q[i] * (float)k[i];
-            s *= a.scale;
+
+    // Tiles are numbered so that sequence b's begin at cu_q[b] / 128 + b: room for any lengths.
+    const int b = wave_find_last(a.B, slot, [&](int s) { return a.cu_q[s] / kPreRows + s; });
+    const int q0 = load_uniform(a.cu_q + b), q1 = load_uniform(a.cu_q + b + 1);
+    const int k0 = load_uniform(a.cu_k + b), k1 = load_uniform(a.cu_k + b + 1);
+    if (!pre_lengths_ok(a, q0, q1, k0, k1)) return;
+    const int lq = q1 - q0, lk = k1 - k0;
+    const int i0 = (slot - (q0 / kPreRows + b)) * kPreRows;  // first query of the workgroup, within the sequence
+    if (i0 < 0 || i0 >= lq) return;
+    const int hk = h / a.G;
+
+    // positions: the workgroup's, the wave's and the lane's queries
+    const int shift = lk - lq;
+    const int wg_hi = min(i0 + kPreRows, lq) + shift;  // first key that no query sees
+    const int wg_lo = a.window ? max(0, i0 + shift - a.window + 1) : 0;
+    const int wi0 = i0 + 32 * wave;
+    const int w_hi = min(wi0 + 32, lq) + shift, w_lo = a.window ? wi0 + shift - a.window + 1 : 0;
+    const int qi = min(wi0 + c, lq - 1);
+    const int see_hi = qi + shift + 1, see_lo = a.window ? see_hi - a.window : 0;
+    const bool idle = wi0 >= lq;
+
+    u32x4 qf[KC];
+    {
+        const uint32_t flip = a.flip > 0 ? 0x80008000u : 0u, keep = a.flip < 0 ? 0u : ~0u;
+        const T *qp = (const T *)a.q + (size_t)(q0 + qi) * a.ldq + (size_t)h * DH + 8 * hf;
+#pragma unroll
+        for (int i = 0; i < KC; ++i) qf[i] = (*(const u32x4 *)(qp + 16 * i) ^ flip) & keep;
+    }
+    f32x16 o[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[i][j] = 0.f;
+    float m = -INFINITY, muse = 0.f, l = 0.f;
+
+    // A tile's copy: each wave takes every fourth KiB; rows behind the last key repeat it.
+    auto copy = [&](int j0, char *sk, char *sv) {
+        constexpr int RPK = 1024 / (DH * 2), KIB = L::BYTES / 1024;  // rows of a KiB
+#pragma unroll
+        for (int i = 0; i < KIB / kPreWaves; ++i) {
+            const int kib = i * kPreWaves + wave;
+            const int r = kib * RPK + lane / L::CH, p = lane % L::CH;
+            const size_t row = (size_t)(k0 + min(j0 + r, lk - 1));
+            global_to_lds16((const T *)a.k + row * a.ldk + hk * DH + 8 * L::k_piece(r, p), sk + kib * 1024);
+            global_to_lds16((const T *)a.v + row * a.ldv + hk * DH + 8 * L::v_piece(r, p), sv + kib * 1024);
         }
-        float top = s;
-        for (int o = 32; o; o >>= 1) top = __builtin_fmaxf(top, shfl_xor(top, o));
-        top = __builtin_fmaxf(top, mx);
-        const float p = s == -INFINITY ? 0.f : expf(s - top), keep = mx == -INFINITY ? 0.f : expf(mx - top);
-        mx = top;
-        l *= keep;
-        for (int i = 0; i < C; ++i) acc[i] *= keep;
-        for (int i = 0; i < 64 && j0 + i < end; ++i) {
-            const float w = __shfl(p, i);
-            const T *v = (const T *)a.v + (size_t)(k0 + j0 + i) * a.ldv + hk * DH;
-            l += w;
-            for (int x = 0; x < C; ++x) acc[x] += w * (float)v[lane + 64 * x];
+    };
+
+    auto use = [&](int j0, const char *sk, const char *sv) {
+        if (idle || j0 >= w_hi || j0 + N <= w_lo) return;
+        f32x16 s[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) s[n][j] = 0.f;
+#pragma unroll
+        for (int i = 0; i < KC; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int r = 32 * n + c;
+                s[n] = E::mfma(*(const u32x4 *)(sk + r * DH * 2 + 16 * L::k_piece(r, 2 * i + hf)), qf[i], s[n]);
+            }
+        // register 4 x + y of tile n: key 32 n + 8 x + 4 hf + y
+        if (j0 + N > wi0 + shift + 1 || (a.window && j0 < w_hi - a.window)) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const int key = j0 + 32 * n + 8 * (j / 4) + 4 * hf + j % 4;
+                    if (key >= see_hi || key < see_lo) s[n][j] = -INFINITY;
+                }
+        }
+        float mt = s[0][0];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) mt = __builtin_fmaxf(mt, s[n][j]);
+        mt = half_max(mt) * a.scale;
+        if (__ballot(mt > m + kPreSlack)) {
+            const float mn = __builtin_fmaxf(m, mt);
+            muse = mn == -INFINITY ? 0.f : mn;
+            const float keep = __builtin_amdgcn_exp2f(m - muse);
+            m = mn;
+            l *= keep;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) o[i] *= keep;
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                s[n][j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][j], a.scale, -muse));
+                l += s[n][j];
+            }
+#pragma unroll
+            for (int kc = 0; kc < 2; ++kc) {
+                u32x4 pf;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) pf[j] = E::pack(s[n][8 * kc + 2 * j], s[n][8 * kc + 2 * j + 1]);
+                const int r = 32 * n + 16 * kc + 4 * hf + (lane & 15) / 4;  // and r + 8
+#pragma unroll
+                for (int mt_ = 0; mt_ < MT; ++mt_) {
+                    const int p = 4 * mt_ + 2 * (c >> 4) + (lane & 3) / 2;
+                    const char *at = sv + r * DH * 2 + 16 * L::v_piece(r, p) + 8 * (lane & 1);
+                    const u32x2 x = lds_read_column4(at), y = lds_read_column4(at + 8 * DH * 2);
+                    o[mt_] = E::mfma(u32x4{x[0], x[1], y[0], y[1]}, pf, o[mt_]);
+                }
+            }
+        }
+    };
+
+    const int first = wg_lo / N * N;
+    if (wg_hi > first) {
+        copy(first, sk0, sv0);
+        for (int j = first; j < wg_hi; j += 2 * N) {
+            wait_vmem_all();
+            __syncthreads();
+            if (j + N < wg_hi) copy(j + N, sk1, sv1);
+            use(j, sk0, sv0);
+            if (j + N >= wg_hi) break;
+            wait_vmem_all();
+            __syncthreads();
+            if (j + 2 * N < wg_hi) copy(j + 2 * N, sk0, sv0);
+            use(j + N, sk1, sv1);
         }
     }
-    T *y = (T *)a.y + ((size_t)row * a.H + h) * DH;
-    for (int x = 0; x < C; ++x) y[lane + 64 * x] = (T)(l > 0.f ? acc[x] / l : 0.f);
+    if (wi0 + c >= lq) return;
+    l += shfl_xor(l, 32);
+    const float f = l > 0.f ? 1.f / l : 0.f;
+    T *y = (T *)a.y + ((size_t)(q0 + wi0 + c) * a.H + h) * DH;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const u32x2 w = {E::pack(o[i][4 * x] * f, o[i][4 * x + 1] * f),
+                             E::pack(o[i][4 * x + 2] * f, o[i][4 * x + 3] * f)};
+            *(u32x2 *)(y + 32 * i + 8 * x + 4 * hf) = w;
+        }
+}
+
+template <int TYPE, int DH>
+static int launch_prefill_dh(const PrefillArgs &a, hipStream_t stream) {
+    hipLaunchKernelGGL((attn_prefill_kernel<TYPE, DH>), dim3((unsigned)((long long)a.slots * a.H)),
+                       dim3(kPreWaves * kWave), 0, stream, a);
+    return hipGetLastError() == hipSuccess ? QG_OK : QG_ERR_LAUNCH;
 }
 
 template <int TYPE>
 static int launch_prefill(const PrefillArgs &a, int Dh, hipStream_t stream) {
-    const dim3 grid(a.nq, a.H);
     switch (Dh) {
-        case 64: hipLaunchKernelGGL((attn_prefill_simple_kernel<TYPE, 64>), grid, dim3(64), 0, stream, a); break;
-        case 128: hipLaunchKernelGGL((attn_prefill_simple_kernel<TYPE, 128>), grid, dim3(64), 0, stream, a); break;
-        default: hipLaunchKernelGGL((attn_prefill_simple_kernel<TYPE, 256>), grid, dim3(64), 0, stream, a); break;
+        case 64: return launch_prefill_dh<TYPE, 64>(a, stream);
+        case 128: return launch_prefill_dh<TYPE, 128>(a, stream);
+        default: return launch_prefill_dh<TYPE, 256>(a, stream);
     }
-    return hipGetLastError() == hipSuccess ? QG_OK : QG_ERR_LAUNCH;
 }
 
 }  // namespace qg
@@ -85,7 +288,11 @@ extern "C" int attn_prefill(int type, const void *q, int ldq, const void *k, int
         return QG_ERR_SHAPE;
     if (((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)y) & 15) return QG_ERR_ALIGN;
     if (((uintptr_t)cu_q | (uintptr_t)cu_k | (uintptr_t)d_status) & 3) return QG_ERR_ALIGN;
-    const PrefillArgs a{q, k, v, y, cu_q, cu_k, d_status, ldq, ldk, ldv, nq, nk, B, H, H / Hkv, window, scale};
+    PrefillArgs a{q, k, v, y, cu_q, cu_k, d_status, ldq, ldk, ldv, nq, nk, B, H, H / Hkv, window};
+    a.scale = scale == 0.f ? 1.f : __builtin_fabsf(scale) * 1.44269504088896340736f;
+    a.flip = scale == 0.f ? -1 : scale < 0.f;
+    a.slots = nq / kPreRows + B;
+    if ((long long)a.slots * H > 0x7fffffffLL) return QG_ERR_SHAPE;
     clear_stale_error();
     if (type == QG_TYPE_F16) return launch_prefill<QG_TYPE_F16>(a, Dh, (hipStream_t)stream);
     return launch_prefill<QG_TYPE_BF16>(a, Dh, (hipStream_t)stream);
