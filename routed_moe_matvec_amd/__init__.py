@@ -262,58 +262,73 @@ def moe_routed_qgemv_noalloc(fmt: int, qx, dx, sx, T: int, D: int, F: int, E: in
 # The attention calls take rows that may be further apart than they are wide
 # (parts of a fused projection), so they check each tensor against the sizes
 # that the kernels will use.
-_TYPE_NAMES = {TYPE_F32: "torch.float32", TYPE_F16: "torch.float16", TYPE_BF16: "torch.bfloat16"}
+if "torch" in globals():
+    _Tensor, _cur_device = torch.Tensor, torch.cuda.current_device
+    # the current stream's handle without a Stream object around it (0.1 us, not 2.8)
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _TYPES = {TYPE_F32: torch.float32, TYPE_F16: torch.float16, TYPE_BF16: torch.bfloat16}
+    _I32, _FP32 = torch.int32, torch.float32
+else:
+    _Tensor, _TYPES, _I32, _FP32 = None, {}, None, None
 
 
 def _rows_ptr(t, name: str, type: int, rows: int, width: int, ld: int):
     """Device pointer of `rows` rows of `width` elements, `ld` elements apart."""
-    if t is None or not hasattr(t, "data_ptr"):
+    if not isinstance(t, _Tensor or ()):
         return _ptr(t)
     if not t.is_cuda:
         raise TypeError("libqgemv takes device tensors; got %s on %s" % (name, t.device))
-    if type in _TYPE_NAMES and str(t.dtype) != _TYPE_NAMES[type]:
-        raise TypeError("%s is %s, the call's type is %s" % (name, t.dtype, _TYPE_NAMES[type]))
-    n = t.shape[0] if t.dim() else 0
-    dense = t.is_contiguous() or (n > 0 and t[0].is_contiguous())
-    each = t.numel() // n if n else 0
-    if t.is_contiguous() and each != width:  # a flat or differently folded tensor
-        have, step = t.numel(), ld
-        fits = have >= (rows - 1) * ld + width
+    if t.dtype is not _TYPES.get(type, t.dtype):
+        raise TypeError("%s is %s, the call's type is %s" % (name, t.dtype, _TYPES[type]))
+    if t.is_contiguous():  # folded in any way
+        n = t.shape[0] if t.dim() else 0
+        fits = ((rows - 1) * ld + width <= t.numel() if n == 0 or t.numel() != n * width
+                else rows <= n and (ld == width or rows <= 1))
     else:
-        step = t.stride(0) if n > 1 else ld
-        fits = dense and each == width and n >= rows
-    if not fits or step != ld:
+        n = t.shape[0]
+        fits = n >= rows and t[0].is_contiguous() and t.numel() == n * width and (t.stride(0) == ld or n == 1)
+    if not fits:
         raise ValueError("%s: %d rows of %d elements, %d apart, do not lie in a tensor of shape %s and strides %s" % (
             name, rows, width, ld, tuple(t.shape), tuple(t.stride())))
     return t.data_ptr()
 
 
-def _array_ptr(t, name: str, dtype: str, count: int):
+def _array_ptr(t, name: str, dtype, count: int):
     """Device pointer of a dense tensor that holds `count` values of dtype (None: any type, counted in bytes)."""
-    if t is None or not hasattr(t, "data_ptr"):
+    if not isinstance(t, _Tensor or ()):
         return _ptr(t)
-    have = t.numel() if dtype else t.numel() * t.element_size()
-    if dtype and str(t.dtype) != "torch." + dtype:
-        raise TypeError("%s is %s, not torch.%s" % (name, t.dtype, dtype))
+    have = t.numel()
+    if dtype is None:
+        have *= t.element_size()
+    elif t.dtype is not dtype:
+        raise TypeError("%s is %s, not %s" % (name, t.dtype, dtype))
     if have < count:
         raise ValueError("%s holds %d, the call needs %d" % (name, have, count))
-    return _ptr(t)
+    if not (t.is_cuda and t.is_contiguous()):
+        return _ptr(t)
+    return t.data_ptr()
 
 
 def _call_on(what: str, f, first, args, stream):
     """f(*args, stream) with the device of tensor `first` current, as its launch needs."""
-    if hasattr(first, "device"):
-        import torch
-        if first.device.index != torch.cuda.current_device():
-            with torch.cuda.device(first.device):
-                _ok(f(*args, _stream(stream, first)), what)
-            return
-    _ok(f(*args, _stream(stream, first)), what)
+    if isinstance(first, _Tensor or ()):
+        dev = first.device
+        if dev.index != _cur_device():
+            with torch.cuda.device(dev):
+                rc = f(*args, _stream(stream, first))
+        else:
+            rc = f(*args, _raw_stream(dev.index) if stream is None else _stream(stream))
+    else:
+        rc = f(*args, _stream(stream))
+    if rc:
+        raise QGError(rc, what)
 
 
 def _cache_args(pages, B: int, max_pages: int, page: int, num_pages: int, Hkv: int, Dh: int, kv):
-    return (_array_ptr(pages, "pages", "int32", B * max_pages), max_pages, page, num_pages,
-            _array_ptr(kv, "kv", None, num_pages * kv4_page_bytes(page, Hkv, Dh)))
+    each = Hkv * page * Dh // 16 * 17 if page & (page - 1) == 0 else 0  # other sizes are the library's to refuse
+    return (_array_ptr(pages, "pages", _I32, B * max_pages), max_pages, page, num_pages,
+            _array_ptr(kv, "kv", None, num_pages * each))
 
 
 def kv4_page_bytes(page: int, Hkv: int, Dh: int) -> int:
@@ -324,9 +339,9 @@ def _kv4(what, f, type, k, ldk, v, ldv, n, cu, lens, B, Hkv, Dh, pages, max_page
          stream):
     w = Hkv * Dh
     _call_on(what, f, k, (type, _rows_ptr(k, "k", type, n, w, ldk), ldk, _rows_ptr(v, "v", type, n, w, ldv), ldv, n,
-                          _array_ptr(cu, "cu", "int32", B + 1), _array_ptr(lens, "lens", "int32", B), B, Hkv, Dh,
+                          _array_ptr(cu, "cu", _I32, B + 1), _array_ptr(lens, "lens", _I32, B), B, Hkv, Dh,
                           *_cache_args(pages, B, max_pages, page, num_pages, Hkv, Dh, kv),
-                          _array_ptr(d_status, "d_status", "int32", 1)), stream)
+                          _array_ptr(d_status, "d_status", _I32, 1)), stream)
 
 
 def kv4_append(type: int, k, ldk: int, v, ldv: int, n: int, cu, lens, B: int, Hkv: int, Dh: int, pages,
@@ -349,10 +364,10 @@ def attn_decode_kv4(type: int, q, ldq: int, lens, B: int, Tq: int, H: int, Hkv: 
                     window: int, max_len: int, pages, max_pages: int, page: int, num_pages: int, kv, y, ws,
                     ws_bytes: int, d_status, stream=None) -> None:
     _call_on("attn_decode_kv4", _c_decode, q,
-             (type, _rows_ptr(q, "q", type, B * Tq, H * Dh, ldq), ldq, _array_ptr(lens, "lens", "int32", B), B, Tq, H,
+             (type, _rows_ptr(q, "q", type, B * Tq, H * Dh, ldq), ldq, _array_ptr(lens, "lens", _I32, B), B, Tq, H,
               Hkv, Dh, scale, window, max_len, *_cache_args(pages, B, max_pages, page, num_pages, Hkv, Dh, kv),
-              _array_ptr(y, "y", "float32", B * Tq * H * Dh), _array_ptr(ws, "ws", None, ws_bytes), ws_bytes,
-              _array_ptr(d_status, "d_status", "int32", 1)), stream)
+              _array_ptr(y, "y", _FP32, B * Tq * H * Dh), _array_ptr(ws, "ws", None, ws_bytes), ws_bytes,
+              _array_ptr(d_status, "d_status", _I32, 1)), stream)
 
 
 def attn_prefill(type: int, q, ldq: int, k, ldk: int, v, ldv: int, nq: int, nk: int, cu_q, cu_k, B: int, H: int,
@@ -360,6 +375,6 @@ def attn_prefill(type: int, q, ldq: int, k, ldk: int, v, ldv: int, nq: int, nk: 
     w = Hkv * Dh
     _call_on("attn_prefill", _c_attn_prefill, q,
              (type, _rows_ptr(q, "q", type, nq, H * Dh, ldq), ldq, _rows_ptr(k, "k", type, nk, w, ldk), ldk,
-              _rows_ptr(v, "v", type, nk, w, ldv), ldv, nq, nk, _array_ptr(cu_q, "cu_q", "int32", B + 1),
-              _array_ptr(cu_k, "cu_k", "int32", B + 1), B, H, Hkv, Dh, scale, window,
-              _rows_ptr(y, "y", type, nq, H * Dh, H * Dh), _array_ptr(d_status, "d_status", "int32", 1)), stream)
+              _rows_ptr(v, "v", type, nk, w, ldv), ldv, nq, nk, _array_ptr(cu_q, "cu_q", _I32, B + 1),
+              _array_ptr(cu_k, "cu_k", _I32, B + 1), B, H, Hkv, Dh, scale, window,
+              _rows_ptr(y, "y", type, nq, H * Dh, H * Dh), _array_ptr(d_status, "d_status", _I32, 1)), stream)

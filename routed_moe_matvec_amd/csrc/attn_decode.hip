@@ -14,6 +14,8 @@
 // hardware conversion takes the UE8M0 scale along), fp32 queries go in as
 // three bf16 parts (24 bits, exact) and fp16 ones as two, weights as two parts
 // (16 bits).  Products and sums are fp32.
+#include <type_traits>
+
 #include "common.h"
 #include "kv4_device.h"
 
@@ -21,27 +23,43 @@ namespace qg {
 
 constexpr int kDecWaves = 4;
 constexpr int kDecStep = 32;                      // positions a wave takes at a time
-constexpr int kDecChunkMin = 256, kDecChunkMax = 4096;  // positions a workgroup takes
-constexpr int kDecMaxPages = kDecChunkMax / 16 + 1;
+constexpr int kDecChunkMax = 8192;                // most positions of a workgroup (4096 times 128 / 64)
 constexpr float kDecSlack = 8.f;                  // a weight may reach 2^8 before the sums are rescaled
 
-// Positions per workgroup of a sequence of which n are visible: about
-// 8 sqrt(n), so that short sequences still spread over the card and long ones
-// do not spend their time joining.  A function of the sequence alone: its
+// Positions per workgroup, as a power of two, of a sequence of which n are
+// visible: about 8 sqrt(n) at 128 channels (as many bytes at 64 and 256), so
+// that short sequences still spread over the card and long ones do not spend
+// their time joining; and 64 a query row, up to 1024, since every row adds
+// Dh sums to what a chunk writes and the join reads (32 sequences with 16 rows
+// of 256 channels: 100 us with 1024, 112 with 512; one such sequence of 8000: 22
+// and 17 us).  A function of the sequence and the heads alone: a sequence's
 // result is the same in any batch.
-__host__ __device__ inline int dec_chunk(int n) {
-    int c = kDecChunkMin;
-    while (c < kDecChunkMax && n >= c / 16 * c) c *= 2;
-    return c;
-}
-__host__ __device__ inline int dec_chunks(int n) { return (n + dec_chunk(n) - 1) / dec_chunk(n); }
+struct DecSplit {
+    int dh_log2, least;  // log2 of the channels, least log2 of a chunk
+    __host__ __device__ int chunk_log2(int n) const {
+        int lg = 8;
+        while (lg < 12 && n >= grows_at(lg)) ++lg;
+        lg += 7 - dh_log2;
+        return lg < least ? least : lg;
+    }
+    __host__ __device__ int grows_at(int lg) const { return 1 << (2 * lg - 5 + 7 - dh_log2); }
+    __host__ __device__ int chunks(int n) const {
+        const int lg = chunk_log2(n);
+        return (n + (1 << lg) - 1) >> lg;
+    }
+    // Most chunks of any n up to `most`: at `most` or just before a chunk grows.
+    int chunks_max(int most) const {
+        int best = chunks(most);
+        for (int lg = 8; lg < 12; ++lg)
+            if (grows_at(lg) - 1 <= most && chunks(grows_at(lg) - 1) > best) best = chunks(grows_at(lg) - 1);
+        return best < 1 ? 1 : best;
+    }
+};
 
-// Most chunks of any n up to `most`: at `most` or just before a chunk grows.
-inline int dec_chunks_max(int most) {
-    int best = dec_chunks(most);
-    for (int c = kDecChunkMin; c < kDecChunkMax; c *= 2)
-        if (c / 16 * c - 1 <= most && dec_chunks(c / 16 * c - 1) > best) best = dec_chunks(c / 16 * c - 1);
-    return best < 1 ? 1 : best;
+inline DecSplit dec_split(int rows, int Dh) {
+    int least = 8;
+    while (least < 10 && 1 << least < 64 * rows) ++least;
+    return DecSplit{Dh == 64 ? 6 : Dh == 128 ? 7 : 8, least};
 }
 
 struct DecodeArgs {
@@ -51,7 +69,9 @@ struct DecodeArgs {
     float *po;   // [B, H * Tq, chunks, Dh] partial sums
     f32x2 *pml;  // [B, H * Tq, chunks] maximum (base 2) and sum
     int ldq, Tq, H, G, window, max_len, chunks;
-    float scale_log2;
+    float scale;  // times log2(e), not negative
+    float qsign;  // 1, -1 (a negative scale) or 0 (scale 0)
+    DecSplit split;
 };
 
 // The visible positions of sequence b's queries are inside [begin, len), begin
@@ -67,10 +87,10 @@ __device__ __forceinline__ int dec_range(const DecodeArgs &a, int b, int *len, i
 
 // 8 elements of q as PARTS bf16 vectors whose sum they are.
 template <int PARTS, class T>
-__device__ __forceinline__ void split8(const T *p, bf16x8 (&out)[PARTS]) {
+__device__ __forceinline__ void split8(const Raw8<T> &r, float sign, bf16x8 (&out)[PARTS]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        float x = (float)p[i];
+        float x = elem(r, i) * sign;
 #pragma unroll
         for (int s = 0; s < PARTS; ++s) {
             const bf16_t h = (bf16_t)x;
@@ -84,42 +104,61 @@ __device__ __forceinline__ void split8(const T *p, bf16x8 (&out)[PARTS]) {
 template <int DH>
 struct DecTile {
     static constexpr int KW = DH / 32, VC = DH / 128 < 1 ? 1 : DH / 128;  // dwords of a key, 16-byte pieces of values
+    static constexpr int KS = VC;  // scales of a key
     uint32_t k[KW];
     u32x4 v[VC];
-    uint32_t ks;      // scale bytes of the lane's channels (DH / 4 of them)
+    uint32_t ks[KS];  // scale bytes of the lane's channels (DH / 4 of them)
     uint32_t vs[VC];  // scale bytes of four positions
 };
 
+// Offsets of a lane's parts in a tile; what depends on the tile is uniform.
 template <int DH>
-__device__ __forceinline__ void dec_load(DecTile<DH> &t, const uint8_t *r, int page, int off, int lane) {
-    const int c = lane & 15, g = lane >> 4;
-    const uint8_t *kp = r + (size_t)(off + c) * (DH / 2) + g * (DH / 8);
+struct DecLane {
+    uint32_t k, ks, v, vs;
+    __device__ DecLane(int lane) {
+        const int c = lane & 15, g = lane >> 4, chunk = DH == 64 ? c >> 1 : c;
+        k = c * (DH / 2) + (DH == 64 ? g * 8 : g * 16);
+        ks = c * (DH / 32) + (DH == 64 ? g >> 1 : g);  // 64 channels: two lanes a byte
+        v = (g * (DH / 8) + chunk) * 16;
+        vs = (g * (DH / 32) + (chunk >> 2)) * 4;
+    }
+};
+
+// Through buffer instructions: the base and the tile's offsets are scalars, so
+// that a load costs no vector arithmetic for its address.
+template <int DH>
+__device__ __forceinline__ void dec_load_k(DecTile<DH> &t, uint8_t *r, int page, int off, const DecLane<DH> &ln) {
+    const auto rs = __builtin_amdgcn_make_buffer_rsrc(r, 0, (uint32_t)page * (DH / 16 * 17), 0x00027000);
+    const int ko = off * (DH / 2), so = page * DH + off * (DH / 32);
+    if constexpr (DH == 64) {
+        const u32x2 w = __builtin_amdgcn_raw_buffer_load_b64(rs, ln.k, ko, 0);
+        t.k[0] = w[0], t.k[1] = w[1];
+    } else {
 #pragma unroll
-    for (int i = 0; i < DH / 32; i += (DH == 64 ? 2 : 4)) {
-        if constexpr (DH == 64) {
-            const u32x2 w = *as_global<u32x2>(kp);
-            t.k[0] = w[0], t.k[1] = w[1];
-        } else {
-            const u32x4 w = *as_global<u32x4>(kp + i * 4);
+        for (int i = 0; i < DH / 32; i += 4) {
+            const u32x4 w = __builtin_amdgcn_raw_buffer_load_b128(rs, ln.k + i * 16, ko, 0);
 #pragma unroll
             for (int j = 0; j < 4; ++j) t.k[i + j] = w[j];
         }
     }
-    const uint8_t *ksp = r + (size_t)page * DH + (size_t)(off + c) * (DH / 32);
-    if constexpr (DH == 64) t.ks = *as_global<uint8_t>(ksp + (g >> 1));
-    if constexpr (DH == 128) t.ks = *as_global<uint8_t>(ksp + g);
-    if constexpr (DH == 256) t.ks = *as_global<uint16_t>(ksp + 2 * g);
+#pragma unroll
+    for (int i = 0; i < DecTile<DH>::KS; ++i) t.ks[i] = __builtin_amdgcn_raw_buffer_load_b8(rs, ln.ks + 4 * i, so, 0);
+}
+template <int DH>
+__device__ __forceinline__ void dec_load_v(DecTile<DH> &t, uint8_t *r, int page, int off, const DecLane<DH> &ln) {
+    const auto rs = __builtin_amdgcn_make_buffer_rsrc(r, 0, (uint32_t)page * (DH / 16 * 17), 0x00027000);
+    const int vo = page * (DH / 2) + off * (DH / 2), so = page * (DH + DH / 32) + off * (DH / 32);
 #pragma unroll
     for (int x = 0; x < DecTile<DH>::VC; ++x) {
-        const int chunk = DH == 64 ? c >> 1 : c + 16 * x;
-        t.v[x] = *as_global<u32x4>(r + (size_t)page * (DH / 2) + ((size_t)((off >> 2) + g) * (DH / 8) + chunk) * 16);
-        t.vs[x] = *as_global<uint32_t>(r + (size_t)page * (DH + DH / 32) +
-                                       (((off >> 2) + g) * (DH / 32) + (chunk >> 2)) * 4);
+        t.v[x] = __builtin_amdgcn_raw_buffer_load_b128(rs, ln.v + x * 256, vo, 0);
+        t.vs[x] = __builtin_amdgcn_raw_buffer_load_b32(rs, ln.vs + x * 16, so, 0);
     }
 }
 
+// Scale byte i where the conversion takes its exponent from, bits 23..30 (it
+// reads no others).
 __device__ __forceinline__ float scale_of(uint32_t bytes, int i) {
-    return __builtin_bit_cast(float, (bytes >> (8 * i) & 0xffu) << 23);
+    return __builtin_bit_cast(float, i < 3 ? bytes << (23 - 8 * i) : bytes >> 1);
 }
 
 template <int B>
@@ -146,6 +185,12 @@ __device__ __forceinline__ float row_sum(float x) {
     return x + shfl_xor(x, 32);
 }
 
+// Keeps the loads before it where they are: they would sink to their use.
+__device__ __forceinline__ void stay() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 // Values of two tiles as the A operands of channel pair (2 B, 2 B + 1) of a
 // 16-byte piece: eight positions of either channel.
 template <int B>
@@ -168,91 +213,126 @@ template <int TYPE>
 constexpr int kQParts = TYPE == QG_TYPE_F32 ? 3 : TYPE == QG_TYPE_F16 ? 2 : 1;
 
 template <int TYPE, int DH>
-__global__ __launch_bounds__(kDecWaves *kWave, 2) void attn_decode_kernel(DecodeArgs a) {
+__global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_decode_kernel(DecodeArgs a) {
     typedef typename ElemOf<TYPE>::type T;
     constexpr int QP = kQParts<TYPE>, KC = DH / 32, MT = DH / 16;  // parts of q, key products, channel tiles
-    // 256 channels: the queries' parts (up to 96 registers) stay in LDS, in the room that the join uses at the end
-    constexpr bool QLDS = DH == 256;
-    __shared__ __attribute__((aligned(16))) float so[2][16 * DH];
-    u32x4 *sq = reinterpret_cast<u32x4 *>(&so[0][0]);
+    // queries of more than 16 registers stay in LDS, in the room that the join uses at the end: more waves fit
+    constexpr bool QLDS = QP * KC > 4;
+    constexpr int PER = DH == 64 ? 4 : 8;  // channel tiles joined at a time
+    __shared__ f32x4 so[kDecWaves * PER * kWave];
+    u32x4 *sq = reinterpret_cast<u32x4 *>(&so[0]);
     static_assert(!QLDS || sizeof(so) >= sizeof(u32x4) * QP * KC * kWave, "queries fit the join's room");
     __shared__ f32x2 sml[kDecWaves][16];
-    __shared__ int spage[kDecMaxPages];
+    __shared__ int spage[kDecChunkMax / 16 + 1];
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int hk = blockIdx.x % a.c.Hkv, ci = blockIdx.x / a.c.Hkv, b = blockIdx.z, row0 = blockIdx.y * 16;
+    // sequence by sequence within a chunk number: the workgroups of chunks that a
+    // sequence does not have come last
+    const int hk = blockIdx.x % a.c.Hkv, bi = blockIdx.x / a.c.Hkv, b = bi % a.c.B, ci = bi / a.c.B;
+    const int row0 = blockIdx.y * 16;
     const int R = a.G * a.Tq;
-    int len, begin;
-    int n = dec_range(a, b, &len, &begin);
-    if (n < 0 && ci == 0 && threadIdx.x == 0) kv4_report(a.c.status, QG_DEV_BAD_LENGTH);
-    const int nchunks = n > 0 ? dec_chunks(n) : 0;
-    if (ci > 0 && ci >= nchunks) return;
-
     const int c = lane & 15, g = lane >> 4;
     const int row = row0 + c;
     const bool live = row < R;
-    const int t = live ? row / a.G : 0, h = hk * a.G + (live ? row - t * a.G : 0);
+    int t = 0;  // the row's token and head
+    for (int i = 1; i < a.Tq; ++i) t += live && row >= i * a.G;
+    const int h = hk * a.G + (live ? row - t * a.G : 0);
     const size_t out_row = (size_t)(b * a.Tq + t) * a.H + h;
+
+    // queries as the B operand: row c, for product i channels 8 i + 0..7 of the
+    // lane's (16 g.. of 64, 32 g.. of each 128); requested first, used once the first keys are on their way
+    constexpr int QN = QLDS ? (KC + kDecWaves - 1) / kDecWaves : KC;
+    Raw8<T> qraw[QN];
+    {
+        const T *qp = (const T *)a.q + (size_t)(b * a.Tq + t) * a.ldq + (size_t)h * DH + g * (DH == 64 ? 16 : 32);
+#pragma unroll
+        for (int i = 0; i < QN; ++i) {
+            const int at = QLDS ? min(i * kDecWaves + wave, KC - 1) : i;
+            qraw[i] = load8(qp + at / 4 * 128 + at % 4 * 8);
+        }
+    }
+
+    int len, begin;
+    const int n = dec_range(a, b, &len, &begin);
+    if (n < 0 && ci == 0 && threadIdx.x == 0) kv4_report(a.c.status, QG_DEV_BAD_LENGTH);
+    const int nchunks = n > 0 ? a.split.chunks(n) : 0;
+    if (ci > 0 && ci >= nchunks) return;
     if (nchunks == 0) {
         if (live && wave == 0)
             for (int i = g * 4; i < DH; i += 16) *(f32x4 *)(a.y + out_row * DH + i) = f32x4{0.f, 0.f, 0.f, 0.f};
         return;
     }
-    const int chunk = dec_chunk(n);
-    const int first = begin + ci * chunk, last = min(len, first + chunk);  // this workgroup's positions
-    const int page = 1 << a.c.page_log2, pg0 = first >> a.c.page_log2;
+    const int lg = a.split.chunk_log2(n);
+    const int first = begin + (ci << lg), last = min(len, first + (1 << lg));  // this workgroup's positions
+    const int page = 1 << a.c.page_log2;
+    const int pos = len - a.Tq + t;                       // this row's position
+    const int see_hi = live ? pos + 1 : 0, see_lo = a.window ? max(pos - a.window + 1, 0) : 0;
+    const size_t region = kv4_region_bytes(page, DH);
+    const DecLane<DH> ln(lane);
+
+    // the chunk's page ids, through LDS (read by scalar loads a step ahead they made the kernel 5 to 15% slower)
+    const int pg0 = first >> a.c.page_log2;
     for (int i = threadIdx.x; i <= ((last - 1) >> a.c.page_log2) - pg0; i += kDecWaves * kWave)
         spage[i] = kv4_page_of(a.c, b, pg0 + i);
+    __syncthreads();
 
-    // queries as the B operand: row c, channels g * DH/4 + 8 i + 0..7 for product i
+    // Where a step's two tiles lie; a tile behind the end or on a bad page
+    // reads the chunk's first place, or page 0, instead and is masked.
+    DecTile<DH> cur[2];
+    uint8_t *at_region[2];
+    int at_off[2];
+    bool next_ok[2];
+    auto locate = [&](int j) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int j0 = j + 16 * x, at = j0 < last ? j0 : first;
+            const int id = __builtin_amdgcn_readfirstlane(spage[(at >> a.c.page_log2) - pg0]);
+            next_ok[x] = j0 < last && id >= 0;
+            at_region[x] = a.c.kv + ((size_t)max(id, 0) * a.c.Hkv + hk) * region;
+            at_off[x] = at & (page - 1);
+        }
+    };
+    auto load_k = [&] {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) dec_load_k<DH>(cur[x], at_region[x], page, at_off[x], ln);
+        stay();
+    };
+    auto load_v = [&] {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) dec_load_v<DH>(cur[x], at_region[x], page, at_off[x], ln);
+        stay();
+    };
+    constexpr int kStride = kDecWaves * kDecStep;
+    const int j_first = first + wave * kDecStep;
+    locate(j_first);
+    load_k();
+    load_v();
+
     u32x4 qf[QP][QLDS ? 1 : KC];
-    {
-        const T *qp = (const T *)a.q + (size_t)(b * a.Tq + t) * a.ldq + (size_t)h * DH + g * (DH / 4);
 #pragma unroll
-        for (int i = 0; i < KC; ++i) {
-            if (QLDS && i % kDecWaves != wave) continue;
-            bf16x8 parts[QP];
-            split8<QP>(qp + 8 * i, parts);
+    for (int i = 0; i < QN; ++i) {
+        const int at = QLDS ? i * kDecWaves + wave : i;
+        bf16x8 parts[QP];
+        split8<QP>(qraw[i], a.qsign, parts);
 #pragma unroll
-            for (int s = 0; s < QP; ++s) {
-                if (QLDS)
-                    sq[(s * KC + i) * kWave + lane] = __builtin_bit_cast(u32x4, parts[s]);
-                else
-                    qf[s][i] = __builtin_bit_cast(u32x4, parts[s]);
-            }
+        for (int s = 0; s < QP; ++s) {
+            if (!QLDS)
+                qf[s][QLDS ? 0 : i] = __builtin_bit_cast(u32x4, parts[s]);
+            else if (at < KC)
+                sq[(s * KC + at) * kWave + lane] = __builtin_bit_cast(u32x4, parts[s]);
         }
     }
-    const int pos = len - a.Tq + t;                       // this row's position
-    const int see_hi = live ? pos + 1 : 0, see_lo = a.window ? pos - a.window + 1 : 0;
-    __syncthreads();
+    if (QLDS) lds_barrier();  // keys and values stay in flight
 
     f32x4 o[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     float m = -INFINITY, muse = 0.f, l = 0.f;
-    const size_t region = kv4_region_bytes(page, DH);
 
-    // Loads of a step's two tiles; a tile behind the end or on a bad page
-    // reads the step's (or chunk's) first place instead and is masked.
-    auto load = [&](int j, DecTile<DH> (&tile)[2], bool (&ok)[2]) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int j0 = j + 16 * x;
-            const int at = j0 < last ? j0 : first;
-            const int id = __builtin_amdgcn_readfirstlane(spage[(at >> a.c.page_log2) - pg0]);
-            ok[x] = j0 < last && id >= 0;
-            dec_load<DH>(tile[x], a.c.kv + ((size_t)max(id, 0) * a.c.Hkv + hk) * region, page, at & (page - 1), lane);
-        }
-    };
-    DecTile<DH> cur[2];
-    bool cur_ok[2];
-    const int j_first = first + wave * kDecStep;
-    if (j_first < last) load(j_first, cur, cur_ok);
-    for (int j = j_first; j < last; j += kDecWaves * kDecStep) {
-        DecTile<DH> next[2];
-        bool next_ok[2] = {false, false};
-        const bool more = j + kDecWaves * kDecStep < last;
-        if (more) load(j + kDecWaves * kDecStep, next, next_ok);
-
+    // A step's keys are loaded again as soon as its scores are there, its
+    // values when they are summed: the loads of the next step run beside the
+    // rest of this one, in the same registers.
+    auto step = [&](int j, auto more) {
+        const bool cur_ok[2] = {next_ok[0], next_ok[1]};
         f32x4 s[2];
         int ql = lane;
         if (QLDS) asm volatile("" : "+v"(ql));  // or the reads below move out of the loop, into registers
@@ -265,34 +345,38 @@ __global__ __launch_bounds__(kDecWaves *kWave, 2) void attn_decode_kernel(Decode
             for (int p = 0; p < QP; ++p) qi[p] = QLDS ? sq[(p * KC + i) * kWave + ql] : qf[p][QLDS ? 0 : i];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const float sc = scale_of(cur[x].ks, DH == 256 ? i / 4 : 0);
+                const float sc = scale_of(cur[x].ks[i / 4], 0);
                 const uint32_t w = cur[x].k[i];
                 const u32x4 kf = {fp4_pair<0>(w, sc), fp4_pair<1>(w, sc), fp4_pair<2>(w, sc), fp4_pair<3>(w, sc)};
 #pragma unroll
                 for (int p = 0; p < QP; ++p) s[x] = mfma16(kf, qi[p], s[x]);
             }
         }
-        // base-2 scores; what a row does not see is -inf
-        float sv[8];
-        const bool whole = j + kDecStep <= min(last, len - a.Tq + 1) && cur_ok[0] && cur_ok[1] && !a.window;
+        if constexpr (more.value) {
+            locate(j + kStride);
+            load_k();
+        }
+        // what a row does not see is -inf
+        const bool whole = j + kDecStep <= min(last, len - a.Tq + 1) && cur_ok[0] && cur_ok[1] &&
+                           (!a.window || j >= len - a.window);
+        if (!whole) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+            for (int x = 0; x < 2; ++x) {
+                const uint32_t span = cur_ok[x] ? (uint32_t)max(min(see_hi, last) - see_lo, 0) : 0u;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int jj = j + 16 * x + 4 * g + i;
-                const float v = s[x][i] * a.scale_log2;
-                sv[4 * x + i] = whole || (cur_ok[x] && jj < min(see_hi, last) && jj >= see_lo) ? v : -INFINITY;
+                for (int i = 0; i < 4; ++i)
+                    if ((uint32_t)(j + 16 * x + 4 * g + i - see_lo) >= span) s[x][i] = -INFINITY;
             }
-        float mt = sv[0];
+        }
+        float mt = s[0][0];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) mt = __builtin_fmaxf(mt, sv[i]);
-        mt = row_max(mt);
+        for (int i = 1; i < 8; ++i) mt = __builtin_fmaxf(mt, s[i / 4][i % 4]);
+        mt = row_max(mt) * a.scale;  // in powers of two, as m
         if (__ballot(mt > m + kDecSlack)) {
             const float mn = __builtin_fmaxf(m, mt);
-            const float use = mn == -INFINITY ? 0.f : mn;
-            const float keep = __builtin_amdgcn_exp2f(m - use);
+            muse = mn == -INFINITY ? 0.f : mn;
+            const float keep = __builtin_amdgcn_exp2f(m - muse);
             m = mn;
-            muse = use;
             l *= keep;
 #pragma unroll
             for (int i = 0; i < MT; ++i) o[i] *= keep;
@@ -302,14 +386,16 @@ __global__ __launch_bounds__(kDecWaves *kWave, 2) void attn_decode_kernel(Decode
             float p[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                p[i] = __builtin_amdgcn_exp2f(sv[i] - muse);
+                p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i / 4][i % 4], a.scale, -muse));
                 l += p[i];
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const bf16x2 hi = {(bf16_t)p[2 * i], (bf16_t)p[2 * i + 1]};
-                const bf16x2 lo = {(bf16_t)(p[2 * i] - (float)hi[0]), (bf16_t)(p[2 * i + 1] - (float)hi[1])};
                 pf[0][i] = __builtin_bit_cast(uint32_t, hi);
+                const float h0 = __builtin_bit_cast(float, pf[0][i] << 16);
+                const float h1 = __builtin_bit_cast(float, pf[0][i] & 0xffff0000u);
+                const bf16x2 lo = {(bf16_t)(p[2 * i] - h0), (bf16_t)(p[2 * i + 1] - h1)};
                 pf[1][i] = __builtin_bit_cast(uint32_t, lo);
             }
         }
@@ -347,93 +433,126 @@ __global__ __launch_bounds__(kDecWaves *kWave, 2) void attn_decode_kernel(Decode
             }
 #undef QG_PAIR
         }
-        if (more) {
-#pragma unroll
-            for (int x = 0; x < 2; ++x) cur[x] = next[x], cur_ok[x] = next_ok[x];
-        }
+        if constexpr (more.value) load_v();
+    };
+    // The last step, which loads nothing, apart: loads behind a condition would
+    // make every wait one for all of them.
+    if (j_first < last) {
+        int j = j_first;
+        for (; j + kStride < last; j += kStride) step(j, std::true_type{});
+        step(j, std::false_type{});
     }
 
-    // join the waves: maxima first, then sums pairwise through LDS
+    // join the waves: maxima first, then the sums of PER channel tiles at a
+    // time through LDS, added and written by all threads (one wave writing
+    // alone cost 22 of 117 us with 16 rows of 256 channels a workgroup)
     l = row_sum(l);
     if (g == 0) sml[wave][c] = f32x2{m, l};
     __syncthreads();  // and every wave is done with the queries
-    float mall = -INFINITY;
+    auto joined = [&](int r) {  // maximum and sum of a row
+        float top = -INFINITY, sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kDecWaves; ++w) mall = __builtin_fmaxf(mall, sml[w][c][0]);
-    const float use = mall == -INFINITY ? 0.f : mall;
-    float lall = 0.f;
+        for (int w = 0; w < kDecWaves; ++w) top = __builtin_fmaxf(top, sml[w][r][0]);
 #pragma unroll
-    for (int w = 0; w < kDecWaves; ++w) lall += sml[w][c][1] * __builtin_amdgcn_exp2f(sml[w][c][0] - use);
-    const float keep = __builtin_amdgcn_exp2f(m - use);
-#pragma unroll
-    for (int i = 0; i < MT; ++i) o[i] *= keep;
-#pragma unroll
-    for (int half = kDecWaves / 2; half; half /= 2) {
-        if (wave >= half && wave < 2 * half)
-#pragma unroll
-            for (int i = 0; i < MT; ++i) *(f32x4 *)&so[wave - half][(i * kWave + lane) * 4] = o[i];
-        __syncthreads();
-        if (wave < half)
-#pragma unroll
-            for (int i = 0; i < MT; ++i) o[i] += *(const f32x4 *)&so[wave][(i * kWave + lane) * 4];
-        __syncthreads();
-    }
-    if (wave != 0 || !live) return;
+        for (int w = 0; w < kDecWaves; ++w)
+            sum += sml[w][r][1] * __builtin_amdgcn_exp2f(sml[w][r][0] - (top == -INFINITY ? 0.f : top));
+        return f32x2{top, sum};
+    };
+    const float top = joined(c)[0], keep = __builtin_amdgcn_exp2f(m - (top == -INFINITY ? 0.f : top));
     // o[8 y + i][k]: channel ((16 y + 4 g + k) * 8 + i), or (4 g + k) * 4 + i for 64 channels
-    constexpr int PER = DH == 64 ? 4 : 8;
-    float *dst = a.y + out_row * DH;
-    float f = lall > 0.f ? 1.f / lall : 0.f;
+    const int wk = threadIdx.x & 3, wl = threadIdx.x >> 2, wc = wl & 15, wg = wl >> 4;  // what this thread writes
+    const int wrow = row0 + wc;
+    int wt = 0;
+    for (int i = 1; i < a.Tq; ++i) wt += wrow >= i * a.G;
+    const size_t wout = (size_t)(b * a.Tq + wt) * a.H + hk * a.G + wrow - wt * a.G;
+    const f32x2 ml = joined(wc);
+    float *dst = a.y + wout * DH;
+    float f = ml[1] > 0.f ? 1.f / ml[1] : 0.f;
     if (nchunks > 1) {
-        const size_t at = ((size_t)b * a.H * a.Tq + (size_t)t * a.H + h) * a.chunks + ci;
-        dst = a.po + at * DH;
+        dst = a.po + (wout * a.chunks + ci) * DH;
         f = 1.f;
-        if (g == 0) a.pml[at] = f32x2{mall, lall};
+        if (wrow < R && wg == 0 && wk == 0) a.pml[wout * a.chunks + ci] = ml;
     }
 #pragma unroll
-    for (int y = 0; y < DecTile<DH>::VC; ++y)
+    for (int y = 0; y < DecTile<DH>::VC; ++y) {
+        if (y) __syncthreads();
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int i = 0; i < PER; ++i) so[(wave * PER + i) * kWave + lane] = o[8 * y + i] * keep;
+        __syncthreads();
+        float acc[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            acc[i] = 0.f;
+#pragma unroll
+            for (int w = 0; w < kDecWaves; ++w)
+                acc[i] += reinterpret_cast<const float *>(&so[(w * PER + i) * kWave + wl])[wk];
+        }
+        if (wrow < R)
 #pragma unroll
             for (int i = 0; i < PER; i += 4)
-                *(f32x4 *)(dst + (16 * y + 4 * g + k) * PER + i) =
-                    f32x4{o[8 * y + i][k], o[8 * y + i + 1][k], o[8 * y + i + 2][k], o[8 * y + i + 3][k]} * f;
+                *(f32x4 *)(dst + (16 * y + 4 * wg + wk) * PER + i) =
+                    f32x4{acc[i], acc[i + 1], acc[i + 2], acc[i + 3]} * f;
+    }
 }
 
-// Joins the chunks of sequences that have several: one wave per query row.
+// Joins the chunks of sequences that have several: one workgroup per query
+// row, Dh / 4 lanes a chunk, so that 8 to 16 chunks are read at once (one wave
+// per row with a chunk at a time took 20 us for 64 rows of 64 chunks).
 template <int DH>
 __global__ __launch_bounds__(256) void attn_decode_join_kernel(DecodeArgs a) {
-    const int rows = a.H * a.Tq, b = blockIdx.y, lane = lane_id();
-    const int row = blockIdx.x * 4 + threadIdx.x / kWave;
+    constexpr int LN = DH / 4, NG = 256 / LN;
+    __shared__ __attribute__((aligned(16))) f32x4 so[256];
+    __shared__ float sl[NG];
+    const int rows = a.H * a.Tq, b = blockIdx.y, row = blockIdx.x, tid = threadIdx.x, lane = lane_id();
     int len, begin;
     const int n = dec_range(a, b, &len, &begin);
-    const int nchunks = n > 0 ? dec_chunks(n) : 0;
-    if (nchunks < 2 || row >= rows) return;
+    const int nchunks = n > 0 ? a.split.chunks(n) : 0;
+    if (nchunks < 2) return;
     const size_t at = ((size_t)b * rows + row) * a.chunks;
+    const int grp = tid / LN, ch = tid % LN;
+    // the first pieces are requested before the maximum is known
+    constexpr int PRE = 4;
+    const float *po = a.po + at * DH + ch * 4;
+    f32x4 pre[PRE];
+#pragma unroll
+    for (int x = 0; x < PRE; ++x) pre[x] = *(const f32x4 *)(po + (size_t)min(grp + x * NG, nchunks - 1) * DH);
     float top = -INFINITY;
     for (int i = lane; i < nchunks; i += kWave) top = __builtin_fmaxf(top, a.pml[at + i][0]);
+#pragma unroll
     for (int x = 32; x; x >>= 1) top = __builtin_fmaxf(top, shfl_xor(top, x));
     const float use = top == -INFINITY ? 0.f : top;
-    float l = 0.f, acc[DH / 64] = {};
-    for (int i = 0; i < nchunks; ++i) {
+    float l = 0.f;
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    auto add = [&](int i, f32x4 o) {
         const f32x2 ml = a.pml[at + i];
         const float w = __builtin_amdgcn_exp2f(ml[0] - use);
         l += ml[1] * w;
-        const float *o = a.po + (at + i) * DH + lane * (DH / 64);
+        acc += o * w;
+    };
 #pragma unroll
-        for (int x = 0; x < DH / 64; ++x) acc[x] += o[x] * w;
-    }
-    float *y = a.y + ((size_t)b * rows + row) * DH + lane * (DH / 64);
+    for (int x = 0; x < PRE; ++x)
+        if (grp + x * NG < nchunks) add(grp + x * NG, pre[x]);
+#pragma unroll 4
+    for (int i = grp + PRE * NG; i < nchunks; i += NG) add(i, *(const f32x4 *)(po + (size_t)i * DH));
+    so[tid] = acc;
+    if (ch == 0) sl[grp] = l;
+    __syncthreads();
+    if (tid >= LN) return;
+    l = 0.f;
 #pragma unroll
-    for (int x = 0; x < DH / 64; ++x) y[x] = l > 0.f ? acc[x] / l : 0.f;
+    for (int i = 0; i < NG; ++i) l += sl[i];
+#pragma unroll
+    for (int i = 1; i < NG; ++i) acc += so[i * LN + ch];
+    *(f32x4 *)(a.y + ((size_t)b * rows + row) * DH + ch * 4) = acc * (l > 0.f ? 1.f / l : 0.f);
 }
 
 template <int TYPE, int DH>
 static int launch_decode_dh(const DecodeArgs &a, hipStream_t stream) {
-    const dim3 grid(a.c.Hkv * a.chunks, (a.G * a.Tq + 15) / 16, a.c.B);
+    const dim3 grid((unsigned)((long long)a.c.Hkv * a.c.B * a.chunks), (a.G * a.Tq + 15) / 16);
     hipLaunchKernelGGL((attn_decode_kernel<TYPE, DH>), grid, dim3(kDecWaves * kWave), 0, stream, a);
     if (hipGetLastError() != hipSuccess) return QG_ERR_LAUNCH;
     if (a.chunks == 1) return QG_OK;
-    hipLaunchKernelGGL(attn_decode_join_kernel<DH>, dim3((a.H * a.Tq + 3) / 4, a.c.B), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL(attn_decode_join_kernel<DH>, dim3(a.H * a.Tq, a.c.B), dim3(256), 0, stream, a);
     return hipGetLastError() == hipSuccess ? QG_OK : QG_ERR_LAUNCH;
 }
 
@@ -447,10 +566,10 @@ static int launch_decode(const DecodeArgs &a, int Dh, hipStream_t stream) {
 }
 
 // The workspace: partial sums, then maxima and sums, of every row and chunk.
-static int decode_chunks(int Tq, int max_len, int window) {
+static int decode_chunks(int Tq, int G, int Dh, int max_len, int window) {
     long long most = max_len;
     if (window && (long long)window + Tq - 1 + 15 < most) most = (long long)window + Tq - 1 + 15;
-    return dec_chunks_max((int)most);
+    return dec_split(G * Tq, Dh).chunks_max((int)most);
 }
 static size_t decode_sums_bytes(int B, int Tq, int H, int Dh, int chunks) {
     return (size_t)B * Tq * H * chunks * Dh * sizeof(float);
@@ -466,7 +585,7 @@ static bool decode_shape_ok(int B, int Tq, int H, int Hkv, int Dh, int max_len, 
 
 extern "C" size_t attn_decode_workspace_bytes(int B, int Tq, int H, int Hkv, int Dh, int max_len, int window) {
     if (!qg::decode_shape_ok(B, Tq, H, Hkv, Dh, max_len, window)) return 0;
-    const int chunks = qg::decode_chunks(Tq, max_len, window);
+    const int chunks = qg::decode_chunks(Tq, H / Hkv, Dh, max_len, window);
     if (chunks == 1) return 256;
     return qg::decode_sums_bytes(B, Tq, H, Dh, chunks) + (size_t)B * Tq * H * chunks * 2 * sizeof(float);
 }
@@ -503,11 +622,13 @@ extern "C" int attn_decode_kv4(int type, const void *q, int ldq, const int32_t *
     a.G = H / Hkv;
     a.window = window;
     a.max_len = max_len;
-    a.scale_log2 = scale * 1.44269504088896340736f;
-    a.chunks = decode_chunks(Tq, max_len, window);
+    a.scale = scale == 0.f ? 1.f : __builtin_fabsf(scale) * 1.44269504088896340736f;
+    a.qsign = scale > 0.f ? 1.f : scale < 0.f ? -1.f : 0.f;
+    a.chunks = decode_chunks(Tq, H / Hkv, Dh, max_len, window);
+    a.split = dec_split(a.G * Tq, Dh);
     a.po = (float *)ws;
     a.pml = (f32x2 *)((uint8_t *)ws + (a.chunks == 1 ? 0 : decode_sums_bytes(B, Tq, H, Dh, a.chunks)));
-    if ((long long)Hkv * a.chunks > 0x7fffffffLL) return QG_ERR_SHAPE;
+    if ((long long)Hkv * B * a.chunks > 0x7fffffffLL) return QG_ERR_SHAPE;
     clear_stale_error();
     switch (type) {
         case QG_TYPE_F32: return launch_decode<QG_TYPE_F32>(a, Dh, (hipStream_t)stream);

@@ -71,6 +71,26 @@ __device__ __forceinline__ int kv4_page_of(const Kv4Cache &c, int b, int pg) {
     return -1;
 }
 
+// Eight elements as they lie in memory, and as fp32.
+template <class T>
+struct Raw8 {
+    u32x4 w[sizeof(T) / 2];
+};
+template <class T>
+__device__ __forceinline__ Raw8<T> load8(const T *p) {
+    Raw8<T> r;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = *(const u32x4 *)((const char *)p + 16 * i);
+    return r;
+}
+__device__ __forceinline__ float elem(const Raw8<float> &r, int i) { return __builtin_bit_cast(float, (uint32_t)r.w[i / 4][i % 4]); }
+__device__ __forceinline__ float elem(const Raw8<_Float16> &r, int i) {
+    return (float)__builtin_bit_cast(f16x2, (uint32_t)r.w[0][i / 2])[i % 2];
+}
+__device__ __forceinline__ float elem(const Raw8<bf16_t> &r, int i) {
+    return (float)__builtin_bit_cast(bf16x2, (uint32_t)r.w[0][i / 2])[i % 2];
+}
+
 // Index of the last b in [0, B) with key(b) <= x (0 if none), searched 64 ways
 // at a time by the whole wave: one memory round trip for up to 64 sequences,
 // two for 4096.  x is wave-uniform, key(0) is not read.
