@@ -20,7 +20,6 @@
 namespace qg {
 
 constexpr int kPreWaves = 4;
-constexpr int kPreRows = 32 * kPreWaves;  // queries of a workgroup
 constexpr float kPreSlack = 8.f;          // a weight may reach 2^8 before the sums are rescaled
 
 struct PrefillArgs {
@@ -59,12 +58,15 @@ struct PreElem<QG_TYPE_BF16> {
     }
 };
 
-// Keys of a tile, and where the 16-byte piece p of row r is held: reads of one
-// piece of many rows (keys) or of four pieces of four rows (values) then fall
-// into different banks.
-template <int DH>
+// A workgroup's shape: KS waves share 32 queries, each with its own keys of a
+// tile, so ROWS = 128 / KS queries a workgroup; and where the 16-byte piece p
+// of row r of a tile is held: reads of one piece of many rows (keys) or of four
+// pieces of four rows (values) then fall into different banks.
+template <int DH, int KS>
 struct PreTile {
-    static constexpr int N = DH == 256 ? 32 : 64, CH = DH / 8, BYTES = N * DH * 2;
+    static constexpr int RW = kPreWaves / KS, ROWS = 32 * RW;
+    static constexpr int N = KS == 4 ? 128 : KS == 1 && DH == 256 ? 32 : 64;  // keys
+    static constexpr int CH = DH / 8, BYTES = N * DH * 2;
     __device__ static int k_piece(int r, int p) { return p ^ (r & (CH < 16 ? CH - 1 : 15)); }
     __device__ static int v_piece(int r, int p) { return p ^ (DH == 64 ? (r >> 1 & 1) << 2 : (r & 3) << 2); }
 };
@@ -88,50 +90,135 @@ __device__ __forceinline__ bool pre_lengths_ok(const PrefillArgs &a, int q0, int
     return q0 >= 0 && q1 >= q0 && q1 <= a.nq && k0 >= 0 && k1 >= k0 && k1 <= a.nk;
 }
 
-template <int TYPE, int DH>
-__global__ __launch_bounds__(kPreWaves *kWave, 2) void attn_prefill_kernel(PrefillArgs a) {
+// Sum over the wave, the same in every lane.
+__device__ __forceinline__ int wave_sum(int x) {
+#define QG_DPP_ADD(ctrl, rows) x += __builtin_amdgcn_update_dpp(0, x, ctrl, rows, 0xf, false)
+    QG_DPP_ADD(0x111, 0xf);  // lane shifts by 1, 2, 4, 8 within rows of 16
+    QG_DPP_ADD(0x112, 0xf);
+    QG_DPP_ADD(0x114, 0xf);
+    QG_DPP_ADD(0x118, 0xf);
+    QG_DPP_ADD(0x142, 0xa);  // lane 15 of a row to the next
+    QG_DPP_ADD(0x143, 0xc);  // lane 31 to the upper half
+#undef QG_DPP_ADD
+    return __builtin_amdgcn_readlane(x, 63);
+}
+
+// One workgroup's queries: sequence b's tile t, or nothing.
+struct PreWork {
+    bool any;
+    int q0, q1, k0, k1, t;
+};
+
+// Up to 64 sequences: the tile of the given rank when all are ordered by the
+// keys they see, most first, so that the longest do not start last (six
+// prompts of 1 to 3301 keys: 154 us, and 160 in the order of the sequences).
+// A lane looks after one sequence, whose tiles see one more bucket of ROWS
+// keys each; a bisection over the buckets finds the rank's.
+template <int ROWS>
+__device__ __forceinline__ PreWork pre_by_rank(const PrefillArgs &a, int rank) {
+    const int b = min(lane_id(), a.B - 1);
+    const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
+    int tiles = 0, base = 0;
+    if (lane_id() < a.B && pre_lengths_ok(a, q0, q1, k0, k1)) {
+        tiles = (q1 - q0 + ROWS - 1) / ROWS;
+        base = ((k1 - k0) - (q1 - q0) + QG_MAX_ATTN_TOKENS) / ROWS;  // bucket of tile 0, not negative
+    }
+    PreWork w{false, 0, 0, 0, 0, 0};
+    if (rank >= wave_sum(tiles)) return w;
+    auto at_least = [&](int x) { return wave_sum(min(max(tiles + min(base - x, 0), 0), tiles)); };
+    int lo = 0, hi = 2 * (QG_MAX_ATTN_TOKENS / ROWS) + 2;  // at_least(lo) > rank >= at_least(hi)
+    // mostly among the first sequence's buckets
+    const int own = __builtin_amdgcn_readfirstlane(base), top = own + __builtin_amdgcn_readfirstlane(tiles);
+    if (own > 0) {
+        if (at_least(own) > rank)
+            lo = own;
+        else
+            hi = own;
+        if (top > lo && top < hi) {
+            if (at_least(top) > rank)
+                lo = top;
+            else
+                hi = top;
+        }
+    }
+    while (hi - lo > 1) {
+        const int mid = lo + (hi - lo) / 2;
+        if (at_least(mid) > rank)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const int nth = rank - at_least(lo + 1);
+    const bool has = lo >= base && lo - base < tiles;
+    const unsigned long long mask = __ballot(has);
+    const int before = __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+    const int src = __builtin_ctzll(__ballot(has && before == nth) | 1ull << 63);
+    w.any = true;
+    w.q0 = __builtin_amdgcn_readlane(q0, src);
+    w.q1 = __builtin_amdgcn_readlane(q1, src);
+    w.k0 = __builtin_amdgcn_readlane(k0, src);
+    w.k1 = __builtin_amdgcn_readlane(k1, src);
+    w.t = lo - __builtin_amdgcn_readlane(base, src);
+    return w;
+}
+
+// More sequences: numbered so that sequence b's tiles begin at cu_q[b] / ROWS +
+// b (room for any lengths), the last queries first.
+template <int ROWS>
+__device__ __forceinline__ PreWork pre_by_slot(const PrefillArgs &a, int slot) {
+    const int b = wave_find_last(a.B, slot, [&](int s) { return a.cu_q[s] / ROWS + s; });
+    PreWork w;
+    w.q0 = load_uniform(a.cu_q + b);
+    w.q1 = load_uniform(a.cu_q + b + 1);
+    w.k0 = load_uniform(a.cu_k + b);
+    w.k1 = load_uniform(a.cu_k + b + 1);
+    w.t = slot - (w.q0 / ROWS + b);
+    w.any = pre_lengths_ok(a, w.q0, w.q1, w.k0, w.k1) && w.t >= 0 && w.t * ROWS < w.q1 - w.q0;
+    return w;
+}
+
+template <int TYPE, int DH, int KS>
+__global__ __launch_bounds__(kPreWaves *kWave, DH == 256 || KS > 1 ? 1 : 2) void attn_prefill_kernel(PrefillArgs a) {
     typedef typename ElemOf<TYPE>::type T;
     typedef PreElem<TYPE> E;
-    typedef PreTile<DH> L;
-    constexpr int N = L::N, NT = N / 32, KC = DH / 16, MT = DH / 32;
+    typedef PreTile<DH, KS> L;
+    constexpr int N = L::N, NT = N / 32 / KS, KC = DH / 16, MT = DH / 32;
     // four objects: the compiler tells the copies in flight into one from the reads of another
     __shared__ __attribute__((aligned(16))) char sk0[L::BYTES], sk1[L::BYTES], sv0[L::BYTES], sv1[L::BYTES];
+    __shared__ f32x2 sml[KS][kPreWaves][32];
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int c = lane & 31, hf = lane >> 5;
+    const int c = lane & 31, hf = lane >> 5, rw = KS == 1 ? wave : wave % L::RW;
+    const int ks = KS == 1 ? 0 : wave / L::RW;
 
     // Workgroups are dealt to the 8 XCDs in turn: where the heads divide by 8,
     // each XCD takes its own heads, so a key/value head's tiles are fetched
-    // into one L2.  The last queries of a sequence, which see most, go first.
+    // into one L2.
     const int id = blockIdx.x;
-    int h, slot;
+    int h, rank;
     if (a.H % 8 == 0) {
         const int per = a.H / 8, i = id >> 3;
         h = (id & 7) * per + i % per;
-        slot = a.slots - 1 - i / per;
+        rank = i / per;
     } else {
         h = id % a.H;
-        slot = a.slots - 1 - id / a.H;
+        rank = id / a.H;
     }
     if (id == 0)
         for (int b = threadIdx.x; b < a.B; b += kPreWaves * kWave)
             if (!pre_lengths_ok(a, a.cu_q[b], a.cu_q[b + 1], a.cu_k[b], a.cu_k[b + 1]))
                 kv4_report(a.status, QG_DEV_BAD_LENGTH);
 
-    // Tiles are numbered so that sequence b's begin at cu_q[b] / 128 + b: room for any lengths.
-    const int b = wave_find_last(a.B, slot, [&](int s) { return a.cu_q[s] / kPreRows + s; });
-    const int q0 = load_uniform(a.cu_q + b), q1 = load_uniform(a.cu_q + b + 1);
-    const int k0 = load_uniform(a.cu_k + b), k1 = load_uniform(a.cu_k + b + 1);
-    if (!pre_lengths_ok(a, q0, q1, k0, k1)) return;
-    const int lq = q1 - q0, lk = k1 - k0;
-    const int i0 = (slot - (q0 / kPreRows + b)) * kPreRows;  // first query of the workgroup, within the sequence
-    if (i0 < 0 || i0 >= lq) return;
+    const PreWork w = a.B <= kWave ? pre_by_rank<L::ROWS>(a, rank) : pre_by_slot<L::ROWS>(a, a.slots - 1 - rank);
+    if (!w.any) return;
+    const int q0 = w.q0, k0 = w.k0, lq = w.q1 - q0, lk = w.k1 - k0;
+    const int i0 = w.t * L::ROWS;  // first query of the workgroup, within the sequence
     const int hk = h / a.G;
 
     // positions: the workgroup's, the wave's and the lane's queries
     const int shift = lk - lq;
-    const int wg_hi = min(i0 + kPreRows, lq) + shift;  // first key that no query sees
+    const int wg_hi = min(i0 + L::ROWS, lq) + shift;  // first key that no query sees
     const int wg_lo = a.window ? max(0, i0 + shift - a.window + 1) : 0;
-    const int wi0 = i0 + 32 * wave;
+    const int wi0 = i0 + 32 * rw;
     const int w_hi = min(wi0 + 32, lq) + shift, w_lo = a.window ? wi0 + shift - a.window + 1 : 0;
     const int qi = min(wi0 + c, lq - 1);
     const int see_hi = qi + shift + 1, see_lo = a.window ? see_hi - a.window : 0;
@@ -164,8 +251,10 @@ __global__ __launch_bounds__(kPreWaves *kWave, 2) void attn_prefill_kernel(Prefi
         }
     };
 
-    auto use = [&](int j0, const char *sk, const char *sv) {
-        if (idle || j0 >= w_hi || j0 + N <= w_lo) return;
+    auto use = [&](int tile, const char *sk, const char *sv) {
+        constexpr int OWN = 32 * NT;  // keys of a tile that are this wave's
+        const int r0 = ks * OWN, j0 = tile + r0;
+        if (idle || j0 >= w_hi || j0 + OWN <= w_lo) return;
         f32x16 s[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -175,11 +264,12 @@ __global__ __launch_bounds__(kPreWaves *kWave, 2) void attn_prefill_kernel(Prefi
         for (int i = 0; i < KC; ++i)
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const int r = 32 * n + c;
-                s[n] = E::mfma(*(const u32x4 *)(sk + r * DH * 2 + 16 * L::k_piece(r, 2 * i + hf)), qf[i], s[n]);
+                const int r = r0 + 32 * n + c;
+                const int at = r * DH * 2 + 16 * L::k_piece(r, 2 * i + hf);
+                s[n] = E::mfma(*(const u32x4 *)(sk + at), qf[i], s[n]);
             }
         // register 4 x + y of tile n: key 32 n + 8 x + 4 hf + y
-        if (j0 + N > wi0 + shift + 1 || (a.window && j0 < w_hi - a.window)) {
+        if (j0 + OWN > wi0 + shift + 1 || (a.window && j0 < w_hi - a.window)) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -215,12 +305,12 @@ __global__ __launch_bounds__(kPreWaves *kWave, 2) void attn_prefill_kernel(Prefi
                 u32x4 pf;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) pf[j] = E::pack(s[n][8 * kc + 2 * j], s[n][8 * kc + 2 * j + 1]);
-                const int r = 32 * n + 16 * kc + 4 * hf + (lane & 15) / 4;  // and r + 8
+                const int r = r0 + 32 * n + 16 * kc + 4 * hf + (lane & 15) / 4;  // and r + 8
 #pragma unroll
                 for (int mt_ = 0; mt_ < MT; ++mt_) {
                     const int p = 4 * mt_ + 2 * (c >> 4) + (lane & 3) / 2;
-                    const char *at = sv + r * DH * 2 + 16 * L::v_piece(r, p) + 8 * (lane & 1);
-                    const u32x2 x = lds_read_column4(at), y = lds_read_column4(at + 8 * DH * 2);
+                    const int at = r * DH * 2 + 16 * L::v_piece(r, p) + 8 * (lane & 1);
+                    const u32x2 x = lds_read_column4(sv + at), y = lds_read_column4(sv + (at + 8 * DH * 2));
                     o[mt_] = E::mfma(u32x4{x[0], x[1], y[0], y[1]}, pf, o[mt_]);
                 }
             }
@@ -242,8 +332,42 @@ __global__ __launch_bounds__(kPreWaves *kWave, 2) void attn_prefill_kernel(Prefi
             use(j + N, sk1, sv1);
         }
     }
-    if (wi0 + c >= lq) return;
     l += shfl_xor(l, 32);
+    if constexpr (KS > 1) {  // join the waves that share queries, through the stages
+        if (hf == 0) sml[ks][rw][c] = f32x2{m, l};
+        __syncthreads();
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int x = 0; x < KS; ++x) top = __builtin_fmaxf(top, sml[x][rw][c][0]);
+        const float use_top = top == -INFINITY ? 0.f : top;
+#pragma unroll
+        for (int x = 0; x < KS; ++x) sum += sml[x][rw][c][1] * __builtin_amdgcn_exp2f(sml[x][rw][c][0] - use_top);
+        const float keep = __builtin_amdgcn_exp2f(m - use_top);
+        l = sum;
+        static_assert(L::BYTES >= 32 * DH * 4 && (KS - 1) * L::RW <= 4, "a wave's sums fit one object");
+        auto room = [&](int i) { return (f32x4 *)(i == 0 ? sk0 : i == 1 ? sk1 : i == 2 ? sv0 : sv1); };
+#pragma unroll
+        for (int i = 0; i < MT; ++i) o[i] *= keep;
+        if (ks > 0)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    room((ks - 1) * L::RW + rw)[(4 * i + x) * kWave + lane] =
+                        f32x4{o[i][4 * x], o[i][4 * x + 1], o[i][4 * x + 2], o[i][4 * x + 3]};
+        __syncthreads();
+        if (ks > 0) return;
+        for (int y = 1; y < KS; ++y)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const f32x4 v = room((y - 1) * L::RW + rw)[(4 * i + x) * kWave + lane];
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) o[i][4 * x + z] += v[z];
+                }
+    }
+    if (wi0 + c >= lq) return;
     const float f = l > 0.f ? 1.f / l : 0.f;
     T *y = (T *)a.y + ((size_t)(q0 + wi0 + c) * a.H + h) * DH;
 #pragma unroll
@@ -256,11 +380,25 @@ __global__ __launch_bounds__(kPreWaves *kWave, 2) void attn_prefill_kernel(Prefi
         }
 }
 
+template <int TYPE, int DH, int KS>
+static int launch_prefill_ks(PrefillArgs a, hipStream_t stream) {
+    a.slots = a.nq / PreTile<DH, KS>::ROWS + a.B;
+    const long long grid = (long long)a.slots * a.H;
+    if (grid > 0x7fffffffLL) return QG_ERR_SHAPE;
+    hipLaunchKernelGGL((attn_prefill_kernel<TYPE, DH, KS>), dim3((unsigned)grid), dim3(kPreWaves * kWave), 0, stream, a);
+    return hipGetLastError() == hipSuccess ? QG_OK : QG_ERR_LAUNCH;
+}
+
+// Where tiles of 128 queries would leave compute units without work, the waves
+// of a workgroup share 64 or 32 queries and split the keys (32 heads of 128:
+// 512 queries of 16384 keys 231 us, 303 without; 3 and 20 of 8000 keys 87 and
+// 149; but 16384 queries 2850 us with 64 a workgroup, 2076 with 128).
 template <int TYPE, int DH>
 static int launch_prefill_dh(const PrefillArgs &a, hipStream_t stream) {
-    hipLaunchKernelGGL((attn_prefill_kernel<TYPE, DH>), dim3((unsigned)((long long)a.slots * a.H)),
-                       dim3(kPreWaves * kWave), 0, stream, a);
-    return hipGetLastError() == hipSuccess ? QG_OK : QG_ERR_LAUNCH;
+    const long long cus = device_cu_count();
+    if ((long long)(a.nq / 128 + a.B) * a.H >= cus) return launch_prefill_ks<TYPE, DH, 1>(a, stream);
+    if (DH == 256 || (long long)(a.nq / 64 + a.B) * a.H >= cus) return launch_prefill_ks<TYPE, DH, 2>(a, stream);
+    return launch_prefill_ks<TYPE, DH, DH == 256 ? 2 : 4>(a, stream);
 }
 
 template <int TYPE>
@@ -291,8 +429,6 @@ extern "C" int attn_prefill(int type, const void *q, int ldq, const void *k, int
     PrefillArgs a{q, k, v, y, cu_q, cu_k, d_status, ldq, ldk, ldv, nq, nk, B, H, H / Hkv, window};
     a.scale = scale == 0.f ? 1.f : __builtin_fabsf(scale) * 1.44269504088896340736f;
     a.flip = scale == 0.f ? -1 : scale < 0.f;
-    a.slots = nq / kPreRows + B;
-    if ((long long)a.slots * H > 0x7fffffffLL) return QG_ERR_SHAPE;
     clear_stale_error();
     if (type == QG_TYPE_F16) return launch_prefill<QG_TYPE_F16>(a, Dh, (hipStream_t)stream);
     return launch_prefill<QG_TYPE_BF16>(a, Dh, (hipStream_t)stream);
