@@ -403,13 +403,26 @@ PREFILL_CASES = [
     ([300, 70, 9], [310, 70, 400], 2, 1, 128, 65),
     ([260], [520], 1, 2, 256, 130),
     ([1500], [1500], 2, 1, 128, 0),
+    # enough tiles for one wave per 32 queries, and for two (the cases above: four)
+    ([300, 0, 129, 1, 64], [300, 7, 129, 1, 200], 8, 8, 64, 0),
+    ([300, 0, 129, 1, 64], [300, 7, 129, 1, 200], 4, 16, 128, 0),
+    ([130, 257, 5], [700, 257, 5], 8, 8, 128, 90),
+    ([300, 129, 40], [300, 129, 3], 8, 8, 256, 0),
+    ([511], [900], 4, 8, 64, 0),
+    ([500], [500], 4, 8, 128, 0),
+    ([64, 500], [128, 530], 2, 8, 128, 200),
+    ([330], [331], 4, 8, 256, 0),
+    # 64 sequences and more: the two ways to find a tile
+    ([(7 * i) % 40 for i in range(64)], [(7 * i) % 40 + i % 3 for i in range(64)], 2, 1, 64, 0),
+    ([(11 * i) % 150 for i in range(70)], [(11 * i) % 150 for i in range(70)], 2, 2, 128, 0),
+    ([0] * 64 + [3] + [0] * 100 + [140], [9] * 64 + [5] + [0] * 100 + [200], 8, 4, 64, 17),
 ]
 
 
 @pytest.mark.parametrize("type", [1, 2])
 @pytest.mark.parametrize("lq,lk,G,Hkv,Dh,window", PREFILL_CASES)
 def test_prefill(qg, lq, lk, G, Hkv, Dh, window, type):
-    progress("prefill %s/%s G %d Hkv %d Dh %d window %d type %d" % (lq, lk, G, Hkv, Dh, window, type))
+    progress("prefill %s/%s G %d Hkv %d Dh %d window %d type %d" % (lq[:6], lk[:6], G, Hkv, Dh, window, type))
     H, dt = G * Hkv, ah.TYPES[type]
     q = normal(1, (max(1, sum(lq)), H, Dh), dt)
     k, v = (normal(i, (max(1, sum(lk)), Hkv, Dh), dt) for i in (2, 3))
@@ -453,6 +466,17 @@ def test_prefill_rising_scores(qg):
     for kk in (k, k.flip(0).contiguous()):
         y, _ = prefill(qg, q, kk, v, [n], [n], 2, 1, 1, 64, 0.5, 0)
         check_prefill(y, q, kk, v, [n], [n], 0.5, 0)
+
+
+def test_prefill_largest_sum_of_queries(qg):
+    """Many heads and tokens at once: every tile of a launch of thousands of workgroups is found and written."""
+    progress("prefill many tiles")
+    lens = [1000, 1, 3, 2500, 128, 127, 700]
+    n = sum(lens)
+    q, k, v = (normal(i, (n, h, 64), torch.bfloat16) for i, h in ((1, 24), (2, 3), (3, 3)))
+    y, st = prefill(qg, q, k, v, lens, lens, 2, 24, 3, 64, 0.125, 0)
+    assert int(st) == 0
+    check_prefill(y, q, k, v, lens, lens, 0.125, 0)
 
 
 def test_prefill_data_errors(qg):
