@@ -462,7 +462,8 @@ int qgemm_prefill_ws(int fmt, const void *W, int N, int K, const uint16_t *x_bf1
  * positions, 0 .. len-1; the query at position p sees the keys j <= p, and with
  * window > 0 only those with j > p - window (window = 0: all).  For each query
  *   y = sum_j softmax_j(scale * q . k_j) v_j     over the keys it sees,
- * and y = 0 where it sees none.  |scale| < 2^127.
+ * and y = 0 where it sees none.  |scale| < 2^127, and scores
+ * must stay inside fp32.
  *
  * q, k and v are rows of packed heads, [tokens, heads, Dh], whose rows may be
  * further apart than heads * Dh: ldq, ldk, ldv count elements from one token
@@ -548,9 +549,9 @@ int kv4_gather(int type, void *k, int ldk, void *v, int ldv, int n, const int32_
  * [B * Tq, H * Dh], what quantize_act_q8 takes.  A query at a negative position
  * (lens[b] < Tq) sees nothing.  max_len: a bound on lens that the host knows
  * (the work is laid out for it), at most max_pages * page.
- * q enters as it is and the codes are exact; scores, softmax and sums are fp32, with
- * the weights of the values carried to 16 bits or more: the error is that of
- * fp32 arithmetic (about 1e-6 of the norm).  A sequence's result does not depend on the others.
+ * q and the cached values enter exactly; scores, softmax weights and sums are
+ * fp32: the error is that of fp32 arithmetic (a few 1e-7 of the norm).  A
+ * sequence's result does not depend on the others, nor on max_len.
  * ws: attn_decode_workspace_bytes(B, Tq, H, Hkv, Dh, max_len, window) bytes of
  * device memory, contents ignored and left unspecified; calls that share it
  * must be ordered on one stream.

@@ -281,16 +281,19 @@ def _rows_ptr(t, name: str, type: int, rows: int, width: int, ld: int):
         raise TypeError("libqgemv takes device tensors; got %s on %s" % (name, t.device))
     if t.dtype is not _TYPES.get(type, t.dtype):
         raise TypeError("%s is %s, the call's type is %s" % (name, t.dtype, _TYPES[type]))
-    if t.is_contiguous():  # folded in any way
-        n = t.shape[0] if t.dim() else 0
-        fits = ((rows - 1) * ld + width <= t.numel() if n == 0 or t.numel() != n * width
-                else rows <= n and (ld == width or rows <= 1))
+    have = t.numel()
+    if t.is_contiguous() and (ld == width or have != t.shape[0] * width):  # folded in any way
+        fits = (rows - 1) * ld + width <= have
     else:
-        n = t.shape[0]
-        fits = n >= rows and t[0].is_contiguous() and t.numel() == n * width and (t.stride(0) == ld or n == 1)
+        shape, steps = t.shape, t.stride()
+        fits, each = shape[0] >= rows and (steps[0] == ld or shape[0] == 1), 1
+        for i in range(len(shape) - 1, 0, -1):
+            fits = fits and (steps[i] == each or shape[i] == 1)
+            each *= shape[i]
+        fits = fits and each == width
     if not fits:
         raise ValueError("%s: %d rows of %d elements, %d apart, do not lie in a tensor of shape %s and strides %s" % (
-            name, rows, width, ld, tuple(t.shape), tuple(t.stride())))
+            name, rows, width, ld, tuple(t.shape), t.stride()))
     return t.data_ptr()
 
 

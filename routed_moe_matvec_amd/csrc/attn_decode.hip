@@ -12,8 +12,9 @@
 // exchange with other rows.
 // Operands are bf16: every E2M1 value times a power of two is exact there (the
 // hardware conversion takes the UE8M0 scale along), fp32 queries go in as
-// three bf16 parts (24 bits, exact) and fp16 ones as two, weights as two parts
-// (16 bits).  Products and sums are fp32.
+// three bf16 parts (24 bits, exact) and fp16 ones as two, weights as three
+// (with two the result was off by 2.4e-6 of its norm, ten times as much as with
+// three).  Products and sums are fp32.
 #include <type_traits>
 
 #include "common.h"
@@ -381,7 +382,7 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
 #pragma unroll
             for (int i = 0; i < MT; ++i) o[i] *= keep;
         }
-        u32x4 pf[2];
+        u32x4 pf[3];
         {
             float p[8];
 #pragma unroll
@@ -395,8 +396,13 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
                 pf[0][i] = __builtin_bit_cast(uint32_t, hi);
                 const float h0 = __builtin_bit_cast(float, pf[0][i] << 16);
                 const float h1 = __builtin_bit_cast(float, pf[0][i] & 0xffff0000u);
-                const bf16x2 lo = {(bf16_t)(p[2 * i] - h0), (bf16_t)(p[2 * i + 1] - h1)};
-                pf[1][i] = __builtin_bit_cast(uint32_t, lo);
+                const float l0 = p[2 * i] - h0, l1 = p[2 * i + 1] - h1;
+                const bf16x2 mid = {(bf16_t)l0, (bf16_t)l1};
+                pf[1][i] = __builtin_bit_cast(uint32_t, mid);
+                const float m0 = __builtin_bit_cast(float, pf[1][i] << 16);
+                const float m1 = __builtin_bit_cast(float, pf[1][i] & 0xffff0000u);
+                const bf16x2 lo = {(bf16_t)(l0 - m0), (bf16_t)(l1 - m1)};
+                pf[2][i] = __builtin_bit_cast(uint32_t, lo);
             }
         }
         if (!(j + kDecStep <= last && cur_ok[0] && cur_ok[1])) {  // scales behind the end may be anything: 0 * NaN
@@ -419,12 +425,10 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
                 v1 >>= (c & 1) * 16;
             }
             u32x4 lo, hi;
-#define QG_PAIR(B)                                                   \
-    dec_values<B>(v0, v1, s0, s1, &lo, &hi);                         \
-    o[8 * y + 2 * B] = mfma16(lo, pf[0], o[8 * y + 2 * B]);          \
-    o[8 * y + 2 * B] = mfma16(lo, pf[1], o[8 * y + 2 * B]);          \
-    o[8 * y + 2 * B + 1] = mfma16(hi, pf[0], o[8 * y + 2 * B + 1]);  \
-    o[8 * y + 2 * B + 1] = mfma16(hi, pf[1], o[8 * y + 2 * B + 1]);
+#define QG_PAIR(B)                                                                                       \
+    dec_values<B>(v0, v1, s0, s1, &lo, &hi);                                                             \
+    for (int w = 0; w < 3; ++w) o[8 * y + 2 * B] = mfma16(lo, pf[w], o[8 * y + 2 * B]);                  \
+    for (int w = 0; w < 3; ++w) o[8 * y + 2 * B + 1] = mfma16(hi, pf[w], o[8 * y + 2 * B + 1]);
             QG_PAIR(0)
             QG_PAIR(1)
             if constexpr (DH > 64) {
@@ -620,7 +624,7 @@ extern "C" int attn_decode_kv4(int type, const void *q, int ldq, const int32_t *
     a.Tq = Tq;
     a.H = H;
     a.G = H / Hkv;
-    a.window = window;
+    a.window = window < max_len ? window : 0;  // a window as long as a sequence hides nothing
     a.max_len = max_len;
     a.scale = scale == 0.f ? 1.f : __builtin_fabsf(scale) * 1.44269504088896340736f;
     a.qsign = scale > 0.f ? 1.f : scale < 0.f ? -1.f : 0.f;

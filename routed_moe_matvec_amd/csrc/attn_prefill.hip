@@ -480,7 +480,8 @@ extern "C" int attn_prefill(int type, const void *q, int ldq, const void *k, int
         return QG_ERR_SHAPE;
     if (((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)y) & 15) return QG_ERR_ALIGN;
     if (((uintptr_t)cu_q | (uintptr_t)cu_k | (uintptr_t)d_status) & 3) return QG_ERR_ALIGN;
-    PrefillArgs a{q, k, v, y, cu_q, cu_k, d_status, ldq, ldk, ldv, nq, nk, B, H, H / Hkv, window};
+    PrefillArgs a{q, k, v, y, cu_q, cu_k, d_status, ldq, ldk, ldv, nq, nk, B, H, H / Hkv,
+                  window < nk ? window : 0};  // a window as long as a sequence hides nothing
     a.scale = scale == 0.f ? 1.f : __builtin_fabsf(scale) * 1.44269504088896340736f;
     a.flip = scale == 0.f ? -1 : scale < 0.f;
     clear_stale_error();

@@ -66,6 +66,9 @@ APPEND_CASES = [
     ([7, 300, 64, 65], [3, 299, 0, 2], 3, 256, 64),
     ([1000], [999], 5, 64, 128),
     ([2] * 130, [1] * 130, 1, 64, 16),
+    ([1 + i % 5 for i in range(4200)], [(i % 7) % (1 + i % 5) for i in range(4200)], 1, 64, 16),
+    ([3000, 1700], [3000, 1700], 16, 64, 32),   # two pieces, and two groups, a wave
+    ([9000], [9000], 8, 128, 64),
 ]
 
 
@@ -214,6 +217,14 @@ def test_decode(qg, lens, Tq, G, Hkv, Dh, page, window, type):
     y, st = decode(qg, c, q, type, Tq, H, scale, window)
     assert int(st) == 0
     check_decode(y, c, q, Tq, scale, window)
+
+
+@pytest.mark.parametrize("window", [1 << 30, (1 << 31) - 1, 450, 449])
+def test_decode_windows_as_long_as_the_sequence(qg, window):
+    c = ah.Cache([450, 0, 3], 1, 64, 16, 31).fill(32)
+    q = normal(33, (3 * 16, 2, 64), torch.float32)
+    y, _ = decode(qg, c, q, 0, 16, 2, 0.1, window)
+    check_decode(y, c, q, 16, 0.1, window)
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.05, 8.0])
@@ -456,6 +467,13 @@ def test_prefill_scales(qg, scale, spread):
     check_prefill(y, q, k, v, lens, lens, scale, 0)
 
 
+@pytest.mark.parametrize("window", [(1 << 31) - 1, 200, 199])
+def test_prefill_windows_as_long_as_the_sequence(qg, window):
+    q, k, v = (normal(i, (203, 2, 64), torch.float16) for i in (1, 2, 3))
+    y, _ = prefill(qg, q, k, v, [200, 3], [200, 3], 1, 2, 2, 64, 0.1, window)
+    check_prefill(y, q, k, v, [200, 3], [200, 3], 0.1, window)
+
+
 def test_prefill_rising_scores(qg):
     """Every later key outweighs all before it by far: the running maximum moves at every step."""
     progress("prefill rising scores")
@@ -545,6 +563,7 @@ def test_binding_refuses_what_does_not_fit(qg):
     for bad, err in [(dict(n=9), ValueError), (dict(ldk=256), ValueError), (dict(k=h), TypeError),
                      (dict(B=8), ValueError), (dict(num_pages=2), ValueError), (dict(max_pages=9), ValueError),
                      (dict(lens=i.long()), TypeError), (dict(v=x.transpose(1, 2)), ValueError),
+                     (dict(v=x[:, :, ::2], Hkv=1), ValueError), (dict(k=x[::2], n=4), ValueError),
                      (dict(n=0), qg.QGError), (dict(page=17), qg.QGError)]:
         with pytest.raises(err):
             qg.kv4_append(**{**ok, **bad})
