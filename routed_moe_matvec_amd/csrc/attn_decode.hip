@@ -213,33 +213,50 @@ __device__ __forceinline__ void dec_values(const u32x4 &v0, const u32x4 &v1, con
 template <int TYPE>
 constexpr int kQParts = TYPE == QG_TYPE_F32 ? 3 : TYPE == QG_TYPE_F16 ? 2 : 1;
 
-template <int TYPE, int DH>
+// The value of the lane 8 columns further on, of 16.
+__device__ __forceinline__ float across8(float x) {
+    return __builtin_bit_cast(
+        float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x128, 0xf, 0xf, true));  // row_ror:8
+}
+
+// SLOTS: 2 with fp32 queries and 8 rows or fewer, else 1.  Then the 16 columns
+// of an operand hold each row twice, with two parts of its queries or weights:
+// two products do the work of three.  A score is the sum over a row's two
+// columns (both get it), and so are the sums over values, once, at the end.
+// Matrix and vector instructions of this kernel take their time one after the
+// other (their busy cycles add up to 94 to 99% of all), so fewer products pay:
+// one sequence of 131001 positions, 8 rows a head, 40.1 -> 37.8 us.  With one or
+// two parts of the queries, and only the weights to gain on, it did not: 32
+// sequences of 4 rows in bf16 18.6 -> 18.9 us, of 2 rows in fp16 34.6 -> 34.9.
+template <int TYPE, int DH, int SLOTS>
 __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_decode_kernel(DecodeArgs a) {
     typedef typename ElemOf<TYPE>::type T;
     constexpr int QP = kQParts<TYPE>, KC = DH / 32, MT = DH / 16;  // parts of q, key products, channel tiles
+    constexpr int ROWS = 16 / SLOTS, QO = (QP + SLOTS - 1) / SLOTS, PO = (3 + SLOTS - 1) / SLOTS;  // operands
     // queries of more than 16 registers stay in LDS, in the room that the join uses at the end: more waves fit
-    constexpr bool QLDS = QP * KC > 4;
+    constexpr bool QLDS = QO * KC > 4;
     constexpr int PER = DH == 64 ? 4 : 8;  // channel tiles joined at a time
     __shared__ f32x4 so[kDecWaves * PER * kWave];
     u32x4 *sq = reinterpret_cast<u32x4 *>(&so[0]);
-    static_assert(!QLDS || sizeof(so) >= sizeof(u32x4) * QP * KC * kWave, "queries fit the join's room");
+    static_assert(!QLDS || sizeof(so) >= sizeof(u32x4) * QO * KC * kWave, "queries fit the join's room");
     __shared__ f32x2 sml[kDecWaves][16];
     __shared__ int spage[kDecChunkMax / 16 + 1];
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     // sequence by sequence within a chunk number: the workgroups of chunks that a
     // sequence does not have come last
     const int hk = blockIdx.x % a.c.Hkv, bi = blockIdx.x / a.c.Hkv, b = bi % a.c.B, ci = bi / a.c.B;
-    const int row0 = blockIdx.y * 16;
+    const int row0 = blockIdx.y * ROWS;
     const int R = a.G * a.Tq;
     const int c = lane & 15, g = lane >> 4;
-    const int row = row0 + c;
+    const int row = row0 + c % ROWS;
+    const uint32_t second = c / ROWS ? ~0u : 0u;  // columns of the second, or no, part
     const bool live = row < R;
     int t = 0;  // the row's token and head
     for (int i = 1; i < a.Tq; ++i) t += live && row >= i * a.G;
     const int h = hk * a.G + (live ? row - t * a.G : 0);
     const size_t out_row = (size_t)(b * a.Tq + t) * a.H + h;
 
-    // queries as the B operand: row c, for product i channels 8 i + 0..7 of the
+    // queries as the B operand: column c, for product i channels 8 i + 0..7 of the
     // lane's (16 g.. of 64, 32 g.. of each 128); requested first, used once the first keys are on their way
     constexpr int QN = QLDS ? (KC + kDecWaves - 1) / kDecWaves : KC;
     Raw8<T> qraw[QN];
@@ -308,18 +325,23 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
     load_k();
     load_v();
 
-    u32x4 qf[QP][QLDS ? 1 : KC];
+    u32x4 qf[QO][QLDS ? 1 : KC];
 #pragma unroll
     for (int i = 0; i < QN; ++i) {
         const int at = QLDS ? i * kDecWaves + wave : i;
         bf16x8 parts[QP];
         split8<QP>(qraw[i], a.qsign, parts);
 #pragma unroll
-        for (int s = 0; s < QP; ++s) {
+        for (int y = 0; y < QO; ++y) {
+            u32x4 w = __builtin_bit_cast(u32x4, parts[y * SLOTS]);
+            if (SLOTS == 2) {
+                w &= ~second;
+                if (2 * y + 1 < QP) w |= __builtin_bit_cast(u32x4, parts[2 * y + 1]) & second;
+            }
             if (!QLDS)
-                qf[s][QLDS ? 0 : i] = __builtin_bit_cast(u32x4, parts[s]);
+                qf[y][QLDS ? 0 : i] = w;
             else if (at < KC)
-                sq[(s * KC + at) * kWave + lane] = __builtin_bit_cast(u32x4, parts[s]);
+                sq[(y * KC + at) * kWave + lane] = w;
         }
     }
     if (QLDS) lds_barrier();  // keys and values stay in flight
@@ -341,22 +363,25 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
         for (int x = 0; x < 2; ++x) s[x] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < KC; ++i) {
-            u32x4 qi[QP];
+            u32x4 qi[QO];
 #pragma unroll
-            for (int p = 0; p < QP; ++p) qi[p] = QLDS ? sq[(p * KC + i) * kWave + ql] : qf[p][QLDS ? 0 : i];
+            for (int y = 0; y < QO; ++y) qi[y] = QLDS ? sq[(y * KC + i) * kWave + ql] : qf[y][QLDS ? 0 : i];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const float sc = scale_of(cur[x].ks[i / 4], 0);
                 const uint32_t w = cur[x].k[i];
                 const u32x4 kf = {fp4_pair<0>(w, sc), fp4_pair<1>(w, sc), fp4_pair<2>(w, sc), fp4_pair<3>(w, sc)};
 #pragma unroll
-                for (int p = 0; p < QP; ++p) s[x] = mfma16(kf, qi[p], s[x]);
+                for (int y = 0; y < QO; ++y) s[x] = mfma16(kf, qi[y], s[x]);
             }
         }
         if constexpr (more.value) {
             locate(j + kStride);
             load_k();
         }
+        if constexpr (SLOTS == 2)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[i / 4][i % 4] += across8(s[i / 4][i % 4]);
         // what a row does not see is -inf
         const bool whole = j + kDecStep <= min(last, len - a.Tq + 1) && cur_ok[0] && cur_ok[1] &&
                            (!a.window || j >= len - a.window);
@@ -382,7 +407,7 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
 #pragma unroll
             for (int i = 0; i < MT; ++i) o[i] *= keep;
         }
-        u32x4 pf[3];
+        u32x4 pf[PO];
         {
             float p[8];
 #pragma unroll
@@ -392,17 +417,22 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const bf16x2 hi = {(bf16_t)p[2 * i], (bf16_t)p[2 * i + 1]};
-                pf[0][i] = __builtin_bit_cast(uint32_t, hi);
-                const float h0 = __builtin_bit_cast(float, pf[0][i] << 16);
-                const float h1 = __builtin_bit_cast(float, pf[0][i] & 0xffff0000u);
-                const float l0 = p[2 * i] - h0, l1 = p[2 * i + 1] - h1;
-                const bf16x2 mid = {(bf16_t)l0, (bf16_t)l1};
-                pf[1][i] = __builtin_bit_cast(uint32_t, mid);
-                const float m0 = __builtin_bit_cast(float, pf[1][i] << 16);
-                const float m1 = __builtin_bit_cast(float, pf[1][i] & 0xffff0000u);
-                const bf16x2 lo = {(bf16_t)(l0 - m0), (bf16_t)(l1 - m1)};
-                pf[2][i] = __builtin_bit_cast(uint32_t, lo);
+                float x0 = p[2 * i], x1 = p[2 * i + 1];
+                uint32_t part[3];
+#pragma unroll
+                for (int y = 0; y < 3; ++y) {
+                    part[y] = __builtin_bit_cast(uint32_t, bf16x2{(bf16_t)x0, (bf16_t)x1});
+                    x0 -= __builtin_bit_cast(float, part[y] << 16);
+                    x1 -= __builtin_bit_cast(float, part[y] & 0xffff0000u);
+                }
+#pragma unroll
+                for (int y = 0; y < PO; ++y) {
+                    pf[y][i] = part[y * SLOTS];
+                    if (SLOTS == 2) {
+                        pf[y][i] &= ~second;
+                        if (2 * y + 1 < 3) pf[y][i] |= part[2 * y + 1] & second;
+                    }
+                }
             }
         }
         if (!(j + kDecStep <= last && cur_ok[0] && cur_ok[1])) {  // scales behind the end may be anything: 0 * NaN
@@ -427,8 +457,8 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
             u32x4 lo, hi;
 #define QG_PAIR(B)                                                                                       \
     dec_values<B>(v0, v1, s0, s1, &lo, &hi);                                                             \
-    for (int w = 0; w < 3; ++w) o[8 * y + 2 * B] = mfma16(lo, pf[w], o[8 * y + 2 * B]);                  \
-    for (int w = 0; w < 3; ++w) o[8 * y + 2 * B + 1] = mfma16(hi, pf[w], o[8 * y + 2 * B + 1]);
+    for (int w = 0; w < PO; ++w) o[8 * y + 2 * B] = mfma16(lo, pf[w], o[8 * y + 2 * B]);                 \
+    for (int w = 0; w < PO; ++w) o[8 * y + 2 * B + 1] = mfma16(hi, pf[w], o[8 * y + 2 * B + 1]);
             QG_PAIR(0)
             QG_PAIR(1)
             if constexpr (DH > 64) {
@@ -464,7 +494,10 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
     };
     const float top = joined(c)[0], keep = __builtin_amdgcn_exp2f(m - (top == -INFINITY ? 0.f : top));
     // o[8 y + i][k]: channel ((16 y + 4 g + k) * 8 + i), or (4 g + k) * 4 + i for 64 channels
-    const int wk = threadIdx.x & 3, wl = threadIdx.x >> 2, wc = wl & 15, wg = wl >> 4;  // what this thread writes
+    // what this thread adds and writes: a row's PART tiles from tile wi on, register wk of lane group wg
+    constexpr int PART = PER / SLOTS;
+    const int wk = threadIdx.x & 3, wc = (threadIdx.x >> 2) % ROWS, wg = threadIdx.x >> 6;
+    const int wi = (threadIdx.x >> 2) % 16 / ROWS * PART;
     const int wrow = row0 + wc;
     int wt = 0;
     for (int i = 1; i < a.Tq; ++i) wt += wrow >= i * a.G;
@@ -475,7 +508,7 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
     if (nchunks > 1) {
         dst = a.po + (wout * a.chunks + ci) * DH;
         f = 1.f;
-        if (wrow < R && wg == 0 && wk == 0) a.pml[wout * a.chunks + ci] = ml;
+        if (wrow < R && wg == 0 && wk == 0 && wi == 0) a.pml[wout * a.chunks + ci] = ml;
     }
 #pragma unroll
     for (int y = 0; y < DecTile<DH>::VC; ++y) {
@@ -483,19 +516,28 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
 #pragma unroll
         for (int i = 0; i < PER; ++i) so[(wave * PER + i) * kWave + lane] = o[8 * y + i] * keep;
         __syncthreads();
-        float acc[PER];
+        float acc[PART];
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
+        for (int i = 0; i < PART; ++i) {
             acc[i] = 0.f;
 #pragma unroll
             for (int w = 0; w < kDecWaves; ++w)
-                acc[i] += reinterpret_cast<const float *>(&so[(w * PER + i) * kWave + wl])[wk];
-        }
-        if (wrow < R)
 #pragma unroll
-            for (int i = 0; i < PER; i += 4)
-                *(f32x4 *)(dst + (16 * y + 4 * wg + wk) * PER + i) =
-                    f32x4{acc[i], acc[i + 1], acc[i + 2], acc[i + 3]} * f;
+                for (int x = 0; x < SLOTS; ++x)
+                    acc[i] += reinterpret_cast<const float *>(
+                        &so[(w * PER + wi + i) * kWave + 16 * wg + wc + x * ROWS])[wk];
+            acc[i] *= f;
+        }
+        if (wrow < R) {
+            float *at = dst + (16 * y + 4 * wg + wk) * PER + wi;
+            if constexpr (PART >= 4) {
+#pragma unroll
+                for (int i = 0; i < PART; i += 4)
+                    *(f32x4 *)(at + i) = f32x4{acc[i], acc[i + 1], acc[i + 2], acc[i + 3]};
+            } else {
+                *(f32x2 *)at = f32x2{acc[0], acc[1]};
+            }
+        }
     }
 }
 
@@ -552,8 +594,13 @@ __global__ __launch_bounds__(256) void attn_decode_join_kernel(DecodeArgs a) {
 
 template <int TYPE, int DH>
 static int launch_decode_dh(const DecodeArgs &a, hipStream_t stream) {
-    const dim3 grid((unsigned)((long long)a.c.Hkv * a.c.B * a.chunks), (a.G * a.Tq + 15) / 16);
-    hipLaunchKernelGGL((attn_decode_kernel<TYPE, DH>), grid, dim3(kDecWaves * kWave), 0, stream, a);
+    constexpr int SLOTS = kQParts<TYPE> == 3 ? 2 : 1;
+    const int rows = a.G * a.Tq;
+    const dim3 grid((unsigned)((long long)a.c.Hkv * a.c.B * a.chunks), (rows + 15) / 16), block(kDecWaves * kWave);
+    if (rows <= 16 / SLOTS)
+        hipLaunchKernelGGL((attn_decode_kernel<TYPE, DH, SLOTS>), grid, block, 0, stream, a);
+    else
+        hipLaunchKernelGGL((attn_decode_kernel<TYPE, DH, 1>), grid, block, 0, stream, a);
     if (hipGetLastError() != hipSuccess) return QG_ERR_LAUNCH;
     if (a.chunks == 1) return QG_OK;
     hipLaunchKernelGGL(attn_decode_join_kernel<DH>, dim3(a.H * a.Tq, a.c.B), dim3(256), 0, stream, a);

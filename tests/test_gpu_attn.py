@@ -86,6 +86,36 @@ def test_append_magnitudes(qg, spread):
     append_case(qg, [70, 3], [70, 3], 2, 64, 16, 0, 5, spread)
 
 
+@pytest.mark.parametrize("type", [0, 1, 2])
+@pytest.mark.parametrize("e", [-130, -119, -14, 0, 9, 126])
+def test_append_borders(qg, type, e):
+    """Every border between two codes, both signs, and its neighbours in the type on either side."""
+    progress("append borders e %d type %d" % (e, type))
+    dt = ah.TYPES[type]
+    mids = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 5.99, 0.0, 0.5, 1.0, 3.0], dtype=torch.float64)
+    vals = (mids * 2.0 ** max(e, -149)).to(dt)
+    up = torch.nextafter(vals.float(), torch.tensor(math.inf)) if type == 0 else (vals.view(torch.int16) + 1).view(dt)
+    down = torch.nextafter(vals.float(), torch.tensor(0.0)) if type == 0 else (
+        torch.where(vals.view(torch.int16) > 0, vals.view(torch.int16) - 1, vals.view(torch.int16)).view(dt))
+    x = torch.cat([vals, up.to(dt), down.to(dt)])
+    x = torch.cat([x, -x])
+    x = x[torch.isfinite(x) & (x.double().abs() <= 6 * 2.0**e)]
+    g = np.random.default_rng(1)
+    rows = torch.zeros(48, 1, 64, dtype=dt)
+    for r in range(48):
+        rows[r, 0] = x[torch.from_numpy(g.integers(0, len(x), 64))]
+        rows[r, 0, ::32] = torch.tensor(6 * 2.0**e).to(dt) if 6 * 2.0**e <= torch.finfo(dt).max else x.abs().max()
+    c = ah.Cache([48], 1, 64, 16, 3)
+    pages, mp, pg, np_, kv = c.device()
+    k = rows.cuda()
+    v = k.flip(0).contiguous()
+    st = status()
+    qg.kv4_append(type, k, 64, v, 64, 48, ah.cumulative([48]), c.lens_device(), 1, 1, 64, pages, mp, pg, np_, kv, st)
+    for which, t in ((0, k), (1, v)):
+        c.put(0, which, *ah.quantize(t.double().cpu().numpy()), np.arange(48))
+    assert np.array_equal(host(kv), c.bytes) and int(st) == 0
+
+
 def test_append_rows_apart_and_tokens_of_no_sequence(qg):
     progress("append with gaps")
     append_case(qg, [40, 9], [40, 7], 2, 128, 16, 2, 6, gap=8, first=3, behind=2)
