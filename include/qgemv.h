@@ -470,16 +470,20 @@ int qgemm_prefill_ws(int fmt, const void *W, int N, int K, const uint16_t *x_bf1
  * to the next, so that each may be a part of one fused projection's output
  * (every row 16-byte aligned: base pointers and row strides in bytes are
  * multiples of 16).  Outputs named y are dense.  int32 arrays need 4-byte
- * alignment.  Every sequence's own keys and values must be finite; what lies
- * elsewhere (rows of other sequences, positions behind a sequence, unused pages) may
- * hold anything and has no influence.
+ * alignment.  Keys and values that any query of the call sees must be finite;
+ * what lies elsewhere (rows of other sequences, positions behind a sequence or
+ * before every query's window, unused pages) may hold anything and has no
+ * influence.  Outputs and workspaces overlap no input.  One launch holds fewer
+ * than 2^24 workgroups: beyond B * Hkv or B * H of some millions a call is
+ * refused as QG_ERR_SHAPE.
  *
  * The cache.  Keys and values are held in pages of `page` positions (a power
  * of two, 16 .. QG_MAX_PAGE) of one sequence: `kv` is num_pages pages of
  * kv4_page_bytes(page, Hkv, Dh) bytes, pages int32 [B, max_pages] names the
  * page of each block of positions, lens int32 [B] the positions of each
- * sequence.  Entries of `pages` behind a sequence's last position are not
- * read.  Sequences may share pages that are only read.  Inside a page, head
+ * sequence.  Entries of `pages` behind a sequence's last position, or of
+ * positions that the call does not need (before every window, or not among those
+ * appended or read back), are not read.  Sequences may share pages that are only read.  Inside a page, head
  * after head, one head's region is (P = page, 4-bit codes as in
  * QG_FMT_FP4_E2M1_MX, one UE8M0 scale for 32 channels of one position):
  *   key codes    uint8 [P][Dh/2]         byte i: channels 2i (low nibble), 2i+1
@@ -487,6 +491,7 @@ int qgemm_prefill_ws(int fmt, const void *W, int N, int K, const uint16_t *x_bf1
  *                                        ((t/4 * Dh/8 + c/8) * 4 + t%4) * 4 + c%8/2
  *   key scales   uint8 [P][Dh/32]
  *   value scales uint8 [P/4][Dh/32][4]   position t innermost
+ * with scale bytes 7 .. 253, as kv4_append writes them.
  *
  * Data errors: the calls check lengths, offsets and page ids on the device and
  * set *d_status to QG_DEV_BAD_LENGTH or QG_DEV_BAD_PAGE (the larger one, if
@@ -514,7 +519,7 @@ size_t kv4_page_bytes(int page, int Hkv, int Dh);
  *   code = the E2M1 value nearest to |x| * 2^-e, the even code on a tie, with
  *   the sign bit of x.
  * Every step is exact, so the bytes are determined.  NaN or Inf are outside the
- * contract.  Two new tokens that name the same place (a page that two sequences
+ * contract, and so is |x| >= 3.5 * 2^126, whose nearest value is 2^128.  Two new tokens that name the same place (a page that two sequences
  * of the call share) leave either one's bytes or a mix.
  * Data errors: sequence b is left out if cu[b] < 0, cu[b+1] < cu[b], cu[b+1] > n,
  * lens[b] < its new tokens or lens[b] > max_pages * page (where cu decreases, any other

@@ -284,6 +284,7 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
     const int page = 1 << a.c.page_log2;
     const int pos = len - a.Tq + t;                       // this row's position
     const int see_hi = live ? pos + 1 : 0, see_lo = a.window ? max(pos - a.window + 1, 0) : 0;
+    const int seen = a.window ? len - a.Tq - a.window + 1 : 0;  // the first position that a row sees
     const size_t region = kv4_region_bytes(page, DH);
     const DecLane<DH> ln(lane);
 
@@ -435,11 +436,13 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
                 }
             }
         }
-        if (!(j + kDecStep <= last && cur_ok[0] && cur_ok[1])) {  // scales behind the end may be anything: 0 * NaN
+        // what no row sees may be anything, also its scales: 0 * NaN
+        if (!(j + kDecStep <= last && j >= seen && cur_ok[0] && cur_ok[1])) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const int left = cur_ok[x] ? last - (j + 16 * x + 4 * g) : 0;
-                const uint32_t keep = left >= 4 ? 0xffffffffu : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+                const int at = j + 16 * x + 4 * g, left = cur_ok[x] ? last - at : 0, skip = seen - at;
+                uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+                if (skip > 0) keep = skip >= 4 ? 0u : keep & ~0u << (8 * skip);
 #pragma unroll
                 for (int y = 0; y < DecTile<DH>::VC; ++y) cur[x].vs[y] &= keep;
             }
@@ -679,7 +682,8 @@ extern "C" int attn_decode_kv4(int type, const void *q, int ldq, const int32_t *
     a.split = dec_split(a.G * Tq, Dh);
     a.po = (float *)ws;
     a.pml = (f32x2 *)((uint8_t *)ws + (a.chunks == 1 ? 0 : decode_sums_bytes(B, Tq, H, Dh, a.chunks)));
-    if ((long long)Hkv * B * a.chunks > 0x7fffffffLL) return QG_ERR_SHAPE;
+    if ((long long)Hkv * B * a.chunks * ((a.G * Tq + 15) / 16) > kMaxGroups || (long long)H * Tq * B > kMaxGroups)
+        return QG_ERR_SHAPE;
     clear_stale_error();
     switch (type) {
         case QG_TYPE_F32: return launch_decode<QG_TYPE_F32>(a, Dh, (hipStream_t)stream);

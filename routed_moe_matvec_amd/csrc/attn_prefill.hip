@@ -17,6 +17,8 @@
 // anyway: 2110 -> 2087).
 // Weights are rounded to the 16-bit type for their product with V, as is
 // y: the two roundings are of one size, and scores, maxima and sums are fp32.
+// fp16 weights are 2^11 times as large, below 2^15: those of a long prompt's
+// many far keys would otherwise be subnormal, or 0.
 //
 // One prompt of 16384 tokens, 32 heads of 128 with 8 key heads, bf16: 2.09 ms,
 // 1053 TFLOP/s (a large library product reaches 1219).  The matrix cores are busy
@@ -30,7 +32,6 @@
 namespace qg {
 
 constexpr int kPreWaves = 4;
-constexpr float kPreSlack = 8.f;          // a weight may reach 2^8 before the sums are rescaled
 
 struct PrefillArgs {
     const void *q, *k, *v;
@@ -47,7 +48,7 @@ template <int TYPE>
 struct PreElem;
 template <>
 struct PreElem<QG_TYPE_F16> {
-    typedef f16x8 x8;
+    static constexpr float kShift = 11.f, kSlack = 4.f;  // weights are 2^kShift, up to 2^(kShift + kSlack) before the sums are rescaled
     __device__ static f32x16 mfma(u32x4 a, u32x4 b, f32x16 c) {
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
                                                       0, 0);
@@ -58,7 +59,7 @@ struct PreElem<QG_TYPE_F16> {
 };
 template <>
 struct PreElem<QG_TYPE_BF16> {
-    typedef bf16x8 x8;
+    static constexpr float kShift = 0.f, kSlack = 8.f;
     __device__ static f32x16 mfma(u32x4 a, u32x4 b, f32x16 c) {
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
                                                        0, 0, 0);
@@ -229,10 +230,9 @@ __global__ __launch_bounds__(kPreWaves *kWave, DH == 256 || KS == 4 ? 1 : 2) voi
     const int wg_hi = min(i0 + L::ROWS, lq) + shift;  // first key that no query sees
     const int wg_lo = a.window ? max(0, i0 + shift - a.window + 1) : 0;
     const int wi0 = i0 + 32 * rw;
-    const int w_hi = min(wi0 + 32, lq) + shift, w_lo = a.window ? wi0 + shift - a.window + 1 : 0;
+    const int w_hi = min(wi0 + 32, lq) + shift;
     const int qi = min(wi0 + c, lq - 1);
     const int see_hi = qi + shift + 1, see_lo = a.window ? see_hi - a.window : 0;
-    const bool idle = wi0 >= lq;
 
     u32x4 qf[KC];
     {
@@ -341,11 +341,11 @@ __global__ __launch_bounds__(kPreWaves *kWave, DH == 256 || KS == 4 ? 1 : 2) voi
                 }
         }
         if constexpr (do_s.value) {
-            if (__ballot(mt > m + kPreSlack)) {
-                const float mn = __builtin_fmaxf(m, mt);
-                muse = mn == -INFINITY ? 0.f : mn;
-                const float keep = __builtin_amdgcn_exp2f(m - muse);
+            if (__ballot(mt > m + E::kSlack)) {
+                const float mn = __builtin_fmaxf(m, mt), use = mn == -INFINITY ? 0.f : mn;
+                const float keep = __builtin_amdgcn_exp2f(m - use);
                 m = mn;
+                muse = use - E::kShift;
                 l *= keep;
 #pragma unroll
                 for (int i = 0; i < MT; ++i) o[i] *= keep;
@@ -353,7 +353,7 @@ __global__ __launch_bounds__(kPreWaves *kWave, DH == 256 || KS == 4 ? 1 : 2) voi
         }
     };
     f32x16 sa[NT], sb[NT];
-    const int first = wg_lo / N * N;
+    const int first = wg_lo;  // no key that the first query does not see, so none that no query sees
     if (wg_hi > first) {
         // Before a step its keys (of the next tile) and values have arrived for
         // all waves, and all are done with what the copies begun now replace.
@@ -438,7 +438,7 @@ template <int TYPE, int DH, int KS>
 static int launch_prefill_ks(PrefillArgs a, hipStream_t stream) {
     a.slots = a.nq / PreTile<DH, KS>::ROWS + a.B;
     const long long grid = (long long)a.slots * a.H;
-    if (grid > 0x7fffffffLL) return QG_ERR_SHAPE;
+    if (grid > kMaxGroups) return QG_ERR_SHAPE;
     hipLaunchKernelGGL((attn_prefill_kernel<TYPE, DH, KS>), dim3((unsigned)grid), dim3(kPreWaves * kWave), 0, stream, a);
     return hipGetLastError() == hipSuccess ? QG_OK : QG_ERR_LAUNCH;
 }

@@ -230,7 +230,7 @@ static int kv4_move(int type, void *k, int ldk, void *v, int ldv, int n, const i
     if (!kv4_cache_shape_ok(B, Hkv, Dh, max_pages, page, num_pages)) return QG_ERR_SHAPE;
     if (n < 1 || n > QG_MAX_ATTN_TOKENS || !row_stride_ok(type, ldk, Hkv * Dh) || !row_stride_ok(type, ldv, Hkv * Dh))
         return QG_ERR_SHAPE;
-    if (((long long)(n >> 2) + 2LL * B + 1) * ((Hkv * Dh + 511) / 512) > 0x7fffff00LL) return QG_ERR_SHAPE;
+    if (((long long)(n >> 2) + 2LL * B + 1) * ((Hkv * Dh + 511) / 512) > 4 * kMaxGroups) return QG_ERR_SHAPE;
     if (((uintptr_t)k | (uintptr_t)v | (uintptr_t)kv) & 15) return QG_ERR_ALIGN;
     if (((uintptr_t)cu | (uintptr_t)lens | (uintptr_t)pages | (uintptr_t)d_status) & 3) return QG_ERR_ALIGN;
     Kv4Move a{};

@@ -117,6 +117,9 @@ inline bool kv4_cache_shape_ok(int B, int Hkv, int Dh, int max_pages, int page, 
 
 inline size_t elem_bytes(int type) { return type == QG_TYPE_F32 ? 4 : 2; }
 
+// Most workgroups of 256 threads: a launch holds fewer than 2^32 threads.
+constexpr long long kMaxGroups = (1 << 24) - 1;
+
 // Rows of `width` elements every `ld` elements, each 16-byte aligned.
 inline bool row_stride_ok(int type, int ld, int width) {
     return ld >= width && (size_t)ld * elem_bytes(type) % 16 == 0;

@@ -71,6 +71,18 @@ def test_prefill_refuses(lib):
         assert _call(lib, "attn_prefill", PREFILL_T, {**PREFILL, **change}) == code, change
 
 
+def test_launches_too_large_are_refused(lib):
+    """2^24 workgroups of 256 threads and more."""
+    many = dict(B=65535, Hkv=1024, Dh=256, ldk=1 << 18, ldv=1 << 18)
+    for name in ("kv4_append", "kv4_gather"):
+        assert _call(lib, name, MOVE_T, {**MOVE, **many, "n": 100}) == -2
+    assert _call(lib, "attn_decode_kv4", DECODE_T, {**DECODE, "B": 65535, "H": 512, "Hkv": 512, "ldq": 1 << 16}) == -2
+    long = dict(B=64, max_len=1 << 29, page=65536, max_pages=1 << 13, Tq=16, H=512, Hkv=8, ldq=1 << 16)
+    assert _call(lib, "attn_decode_kv4", DECODE_T, {**DECODE, **long, "ws_bytes": 1 << 62}) == -2
+    assert _call(lib, "attn_prefill", PREFILL_T, {**PREFILL, "B": 65535, "H": 1024, "Hkv": 1024, "ldq": 1 << 17,
+                                                  "ldk": 1 << 17, "ldv": 1 << 17, "nq": 70000, "nk": 70000}) == -2
+
+
 def test_sizes():
     import routed_moe_matvec_amd as qg
     for page, Hkv, Dh in [(16, 1, 64), (64, 8, 128), (65536, 3, 256)]:

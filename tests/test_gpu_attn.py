@@ -294,6 +294,28 @@ def test_decode_is_the_same_alone_and_in_a_batch(qg):
         assert torch.equal(alone[0], y[b]), (b, n)
 
 
+@pytest.mark.parametrize("Tq,Dh,window", [(1, 64, 100), (3, 128, 37), (2, 256, 1), (1, 128, 640)])
+def test_decode_what_lies_before_every_window(qg, Tq, Dh, window):
+    """Positions that no query sees any more: their pages are gone from the table, and in the first page that is still
+    needed they may hold anything."""
+    progress("decode before the window %d Dh %d" % (window, Dh))
+    c = ah.Cache([777, 130, 2000, 33], 2, Dh, 32, 71).fill(72)
+    q = normal(73, (4 * Tq, 6, Dh), torch.float32)
+    first = [max(n - Tq - window + 1, 0) for n in c.lens]
+    hidden = {}
+    for b, at in enumerate(first):
+        gone = torch.arange(c.lens[b], device="cuda") < at
+        hidden[b] = gone
+        for pos in range(at // 32 * 32, at):
+            for which in (0, 1):
+                ah.write(c.bytes, 32, 2, Dh, c.table[b, pos // 32], pos % 32, which, np.full((2, Dh), 15, np.uint8),
+                         np.full((2, Dh // 32), 255, np.uint8))
+        c.table[b, :at // 32] = -1
+    y, st = decode(qg, c, q, 0, Tq, 6, 0.1, window)
+    assert int(st) == 0
+    check_decode(y, c, q, Tq, 0.1, window, hidden)
+
+
 def test_decode_rows_apart(qg):
     c = ah.Cache([100, 7], 2, 64, 16, 51).fill(52)
     q = normal(53, (2, 4, 64), torch.bfloat16)
@@ -502,6 +524,35 @@ def test_prefill_windows_as_long_as_the_sequence(qg, window):
     q, k, v = (normal(i, (203, 2, 64), torch.float16) for i in (1, 2, 3))
     y, _ = prefill(qg, q, k, v, [200, 3], [200, 3], 1, 2, 2, 64, 0.1, window)
     check_prefill(y, q, k, v, [200, 3], [200, 3], 0.1, window)
+
+
+@pytest.mark.parametrize("lq,lk,H,window", [(5, 300, 2, 40), (200, 700, 16, 129), (1, 100, 1, 1), (700, 1000, 64, 77)])
+def test_prefill_keys_that_no_query_sees(qg, lq, lk, H, window):
+    """They come before the first query's window and may be NaN."""
+    progress("prefill unseen keys %d %d window %d" % (lq, lk, window))
+    q, k, v = (normal(i, (n, H, 128), torch.bfloat16) for i, n in ((1, lq), (2, lk), (3, lk)))
+    k[:lk - lq - window + 1] = v[:lk - lq - window + 1] = math.nan
+    y, st = prefill(qg, q, k, v, [lq], [lk], 2, H, H, 128, 0.1, window)
+    assert int(st) == 0
+    clean = [torch.nan_to_num(x) for x in (k, v)]
+    check_prefill(y, q, *clean, [lq], [lk], 0.1, window)
+
+
+@pytest.mark.parametrize("type", [1, 2])
+@pytest.mark.parametrize("H", [1, 64, 256])
+def test_prefill_many_small_weights(qg, H, type):
+    """One key of score 0 and value 0, 4000 of score -17 (a weight of 2^-24.5, between 0 and the type's least in fp16) and
+    value 1.  The rounding of the weights is the same for all 4000, at most half a step, and so is y's: eps / 2 each;
+    fp32 sums of 4001 terms are off by less than 4001 * 2^-24 each, in numerator and denominator."""
+    progress("prefill small weights H %d type %d" % (H, type))
+    n, dt = 4001, ah.TYPES[type]
+    q = torch.zeros(1, H, 64, dtype=dt, device="cuda")
+    k, v = torch.zeros(n, 1, 64, dtype=dt, device="cuda"), torch.ones(n, 1, 64, dtype=dt, device="cuda")
+    q[..., 0], k[1:, :, 0], v[0] = 4.0, -4.25, 0.0
+    y, _ = prefill(qg, q, k, v, [1], [n], type, H, 1, 64, 1.0, 0)
+    w = (n - 1) * math.exp(-17.0)
+    ref = w / (1.0 + w)
+    assert float((y.double() / ref - 1).abs().max()) <= torch.finfo(dt).eps * 1.01 + 2 * n * 2.0**-24
 
 
 def test_prefill_rising_scores(qg):
