@@ -33,12 +33,14 @@ constexpr float kDecSlack = 8.f;                  // a weight may reach 2^8 befo
 // their time joining; and 64 a query row, up to 1024, since every row adds
 // Dh sums to what a chunk writes and the join reads (32 sequences with 16 rows
 // of 256 channels: 100 us with 1024, 112 with 512; one such sequence of 8000: 22
-// and 17 us).  A function of the sequence and the heads alone: a sequence's
-// result is the same in any batch.
+// and 17 us).  Up to 640 positions (of 128 channels) are one chunk, which needs no
+// join (32 query and 8 key heads, one sequence of 640: 8.0 -> 7.6 us, 32 of them 12.6
+// -> 8.8; one of 1024 would go from 8.0 to 10.0).  A function of the sequence and
+// the heads alone: a sequence's result is the same in any batch.
 struct DecSplit {
     int dh_log2, least;  // log2 of the channels, least log2 of a chunk
     __host__ __device__ int chunk_log2(int n) const {
-        int lg = 8;
+        int lg = n <= 5 << (7 + 7 - dh_log2) ? 10 : 8;
         while (lg < 12 && n >= grows_at(lg)) ++lg;
         lg += 7 - dh_log2;
         return lg < least ? least : lg;

@@ -249,6 +249,25 @@ def test_decode(qg, lens, Tq, G, Hkv, Dh, page, window, type):
     check_decode(y, c, q, Tq, scale, window)
 
 
+@pytest.mark.parametrize("Dh,n", [(64, 1280), (128, 640), (256, 320)])
+def test_decode_one_chunk_and_several(qg, Dh, n):
+    """Lengths on both sides of the longest single chunk, in one call; each alone gives the same bits."""
+    progress("decode one chunk Dh %d" % Dh)
+    lens = [n - 1, n, n + 1, 2 * n]
+    c = ah.Cache(lens, 2, Dh, 64, 81).fill(82)
+    q = normal(83, (4, 8, Dh), torch.float32)
+    y, st = decode(qg, c, q, 0, 1, 8, 0.1, 0)
+    assert int(st) == 0
+    check_decode(y, c, q, 1, 0.1, 0)
+    for b in range(4):
+        pages, kv = c.device()[0], c.device()[4]
+        nb = qg.attn_decode_workspace_bytes(1, 1, 8, 2, Dh, lens[b], 0)
+        ws, one, st = torch.empty(nb, dtype=torch.uint8, device="cuda"), torch.empty_like(y[:1]), status()
+        qg.attn_decode_kv4(0, q[b], 8 * Dh, c.lens_device()[b:b + 1], 1, 1, 8, 2, Dh, 0.1, 0, lens[b], pages[b:b + 1],
+                           c.max_pages, 64, c.num_pages, kv, one, ws, nb, st)
+        assert int(st) == 0 and torch.equal(one, y[b:b + 1])
+
+
 @pytest.mark.parametrize("window", [1 << 30, (1 << 31) - 1, 450, 449])
 def test_decode_windows_as_long_as_the_sequence(qg, window):
     c = ah.Cache([450, 0, 3], 1, 64, 16, 31).fill(32)
