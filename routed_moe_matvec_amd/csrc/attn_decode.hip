@@ -226,7 +226,7 @@ __device__ __forceinline__ float across8(float x) {
 // two products do the work of three.  A score is the sum over a row's two
 // columns (both get it), and so are the sums over values, once, at the end.
 // Matrix and vector instructions of this kernel take their time one after the
-// other (their busy cycles add up to 94 to 99% of all), so fewer products pay:
+// other (their busy cycles add up to 85 to 97% of all), so fewer products pay:
 // one sequence of 131001 positions, 8 rows a head, 40.1 -> 37.8 us.  With one or
 // two parts of the queries, and only the weights to gain on, it did not: 32
 // sequences of 4 rows in bf16 18.6 -> 18.9 us, of 2 rows in fp16 34.6 -> 34.9.

@@ -20,8 +20,8 @@
 // fp16 weights are 2^11 times as large, below 2^15: those of a long prompt's
 // many far keys would otherwise be subnormal, or 0.
 //
-// One prompt of 16384 tokens, 32 heads of 128 with 8 key heads, bf16: 2.09 ms,
-// 1053 TFLOP/s (a large library product reaches 1219).  The matrix cores are busy
+// One prompt of 16384 tokens, 32 heads of 128 with 8 key heads, bf16: 2.02 to
+// 2.09 ms, 1053 to 1089 TFLOP/s (a large library product reaches 1219).  The matrix cores are busy
 // 59% of the cycles and the vector units 55%, at a clock that falls as the
 // cycles do (1.9 to 1.7 GHz): the card's power is the limit.
 #include <type_traits>
