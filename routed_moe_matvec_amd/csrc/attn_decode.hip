@@ -364,6 +364,7 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
         if (QLDS) asm volatile("" : "+v"(ql));  // or the reads below move out of the loop, into registers
 #pragma unroll
         for (int x = 0; x < 2; ++x) s[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+        __builtin_amdgcn_s_setprio(1);  // scores before another wave's weights: its loads start earlier (101.7 -> 100.6 us)
 #pragma unroll
         for (int i = 0; i < KC; ++i) {
             u32x4 qi[QO];
@@ -378,6 +379,7 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
                 for (int y = 0; y < QO; ++y) s[x] = mfma16(kf, qi[y], s[x]);
             }
         }
+        __builtin_amdgcn_s_setprio(0);
         if constexpr (more.value) {
             locate(j + kStride);
             load_k();
@@ -423,10 +425,11 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
                 float x0 = p[2 * i], x1 = p[2 * i + 1];
                 uint32_t part[3];
 #pragma unroll
-                for (int y = 0; y < 3; ++y) {
-                    part[y] = __builtin_bit_cast(uint32_t, bf16x2{(bf16_t)x0, (bf16_t)x1});
-                    x0 -= __builtin_bit_cast(float, part[y] << 16);
-                    x1 -= __builtin_bit_cast(float, part[y] & 0xffff0000u);
+                for (int y = 0; y < 3; ++y) {  // eight bits at a time, cut off: no rounding
+                    const uint32_t b0 = __builtin_bit_cast(uint32_t, x0), b1 = __builtin_bit_cast(uint32_t, x1);
+                    part[y] = __builtin_amdgcn_perm(b1, b0, 0x07060302u);
+                    x0 -= __builtin_bit_cast(float, b0 & 0xffff0000u);
+                    x1 -= __builtin_bit_cast(float, b1 & 0xffff0000u);
                 }
 #pragma unroll
                 for (int y = 0; y < PO; ++y) {
@@ -462,8 +465,10 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
             u32x4 lo, hi;
 #define QG_PAIR(B)                                                                                       \
     dec_values<B>(v0, v1, s0, s1, &lo, &hi);                                                             \
-    for (int w = 0; w < PO; ++w) o[8 * y + 2 * B] = mfma16(lo, pf[w], o[8 * y + 2 * B]);                 \
-    for (int w = 0; w < PO; ++w) o[8 * y + 2 * B + 1] = mfma16(hi, pf[w], o[8 * y + 2 * B + 1]);
+    for (int w = 0; w < PO; ++w) {                                                                       \
+        o[8 * y + 2 * B] = mfma16(lo, pf[w], o[8 * y + 2 * B]);                                          \
+        o[8 * y + 2 * B + 1] = mfma16(hi, pf[w], o[8 * y + 2 * B + 1]);                                  \
+    }
             QG_PAIR(0)
             QG_PAIR(1)
             if constexpr (DH > 64) {
