@@ -443,14 +443,19 @@ static int launch_prefill_ks(PrefillArgs a, hipStream_t stream) {
     return hipGetLastError() == hipSuccess ? QG_OK : QG_ERR_LAUNCH;
 }
 
-// Where tiles of 128 queries would leave compute units without work, the waves
-// of a workgroup share 64 or 32 queries and split the keys (32 heads of 128:
-// 512 queries of 16384 keys 231 us, 303 without; 3 and 20 of 8000 keys 87 and
-// 149; but 16384 queries 2850 us with 64 a workgroup, 2076 with 128).
+// Where tiles of 128 queries would fill the card at most once (two workgroups a
+// compute unit, one with 256 channels), the waves of a workgroup share 64 or, where
+// those leave compute units without work, 32 queries and split the keys: smaller
+// tiles also spread the triangle of a prompt more evenly.  32 heads of 128, us with
+// 128, 64, 32 queries: 512 of 16384 keys 303, 231; 3 and 20 of 8000 keys 149, -, 87;
+// prompts of 1024 tokens 28.6, 23.9; 2048 (one round exactly) 56, 57; 3000 94, 106; 16384
+// 2076, 2850; of 768 -, 19, 30.  32 heads of 64: 2048 tokens 36.0, 32.5; 16 heads of
+// 256: 2048 tokens 79, 66; 2500 93, 102.
 template <int TYPE, int DH>
 static int launch_prefill_dh(const PrefillArgs &a, hipStream_t stream) {
-    const long long cus = device_cu_count();
-    if ((long long)(a.nq / 128 + a.B) * a.H >= cus) return launch_prefill_ks<TYPE, DH, 1>(a, stream);
+    const long long cus = device_cu_count(), round = DH == 256 ? cus : 2 * cus;
+    const long long tiles = (long long)(a.nq / 128 + a.B / 2) * a.H;  // a sequence's last tile counted half
+    if (tiles > round || (DH == 128 && tiles == round)) return launch_prefill_ks<TYPE, DH, 1>(a, stream);
     if (DH == 256 || (long long)(a.nq / 64 + a.B) * a.H >= cus) return launch_prefill_ks<TYPE, DH, 2>(a, stream);
     return launch_prefill_ks<TYPE, DH, DH == 256 ? 2 : 4>(a, stream);
 }

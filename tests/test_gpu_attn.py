@@ -514,6 +514,22 @@ def test_prefill(qg, lq, lk, G, Hkv, Dh, window, type):
     check_prefill(y, q, k, v, lq, lk, scale, window)
 
 
+@pytest.mark.parametrize("type", [1, 2])
+@pytest.mark.parametrize("lq,lk,G,Hkv,Dh,window", [
+    ([300, 0, 129, 1, 64], [300, 7, 129, 1, 200], 8, 16, 64, 0),
+    ([300, 0, 129, 1, 64], [300, 7, 129, 1, 200], 8, 16, 128, 0),
+    ([130, 257, 5, 290], [700, 257, 5, 300], 9, 15, 128, 90),
+    ([310, 257, 128], [200, 300, 900], 9, 15, 64, 129),
+    ([300, 129, 140], [300, 129, 3], 8, 8, 256, 0),
+    ([127, 1, 385], [500, 1, 385], 5, 13, 256, 200),
+    ([(11 * i) % 150 for i in range(70)], [(11 * i) % 150 for i in range(70)], 4, 4, 128, 0),
+    ([(11 * i) % 150 for i in range(64)], [(13 * i) % 150 for i in range(64)], 4, 5, 64, 0),
+])
+def test_prefill_tiles_of_128_queries(qg, lq, lk, G, Hkv, Dh, window, type):
+    """Heads and tokens enough for more than one round of full tiles."""
+    test_prefill(qg, lq, lk, G, Hkv, Dh, window, type)
+
+
 @pytest.mark.parametrize("Dh", [64, 128, 256])
 def test_prefill_parts_of_a_fused_projection(qg, Dh):
     """q, k and v as parts of one matrix whose other columns are NaN; packed rows that belong to no sequence are NaN in q, k and v
