@@ -263,19 +263,23 @@ def moe_routed_qgemv_noalloc(fmt: int, qx, dx, sx, T: int, D: int, F: int, E: in
 # (parts of a fused projection), so they check each tensor against the sizes
 # that the kernels will use.
 if "torch" in globals():
-    _Tensor, _cur_device = torch.Tensor, torch.cuda.current_device
+    _Tensor = torch.Tensor
+    # the current device without a check that torch has begun to use one (0.1 us, not 0.3), and
     # the current stream's handle without a Stream object around it (0.1 us, not 2.8)
+    _cur_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                           lambda index: torch.cuda.current_stream(index).cuda_stream)
     _TYPES = {TYPE_F32: torch.float32, TYPE_F16: torch.float16, TYPE_BF16: torch.bfloat16}
     _I32, _FP32 = torch.int32, torch.float32
 else:
-    _Tensor, _TYPES, _I32, _FP32 = None, {}, None, None
+    class _Tensor:  # nothing is one
+        pass
+    _TYPES, _I32, _FP32 = {}, None, None
 
 
 def _rows_ptr(t, name: str, type: int, rows: int, width: int, ld: int):
     """Device pointer of `rows` rows of `width` elements, `ld` elements apart."""
-    if not isinstance(t, _Tensor or ()):
+    if not isinstance(t, _Tensor):
         return _ptr(t)
     if not t.is_cuda:
         raise TypeError("libqgemv takes device tensors; got %s on %s" % (name, t.device))
@@ -299,7 +303,7 @@ def _rows_ptr(t, name: str, type: int, rows: int, width: int, ld: int):
 
 def _array_ptr(t, name: str, dtype, count: int):
     """Device pointer of a dense tensor that holds `count` values of dtype (None: any type, counted in bytes)."""
-    if not isinstance(t, _Tensor or ()):
+    if not isinstance(t, _Tensor):
         return _ptr(t)
     have = t.numel()
     if dtype is None:
@@ -308,20 +312,18 @@ def _array_ptr(t, name: str, dtype, count: int):
         raise TypeError("%s is %s, not %s" % (name, t.dtype, dtype))
     if have < count:
         raise ValueError("%s holds %d, the call needs %d" % (name, have, count))
-    if not (t.is_cuda and t.is_contiguous()):
-        return _ptr(t)
-    return t.data_ptr()
+    return t.data_ptr() if t.is_cuda and t.is_contiguous() else _ptr(t)
 
 
 def _call_on(what: str, f, first, args, stream):
     """f(*args, stream) with the device of tensor `first` current, as its launch needs."""
-    if isinstance(first, _Tensor or ()):
-        dev = first.device
-        if dev.index != _cur_device():
-            with torch.cuda.device(dev):
+    if isinstance(first, _Tensor):
+        index = first.get_device()
+        if index != _cur_device():
+            with torch.cuda.device(index):
                 rc = f(*args, _stream(stream, first))
         else:
-            rc = f(*args, _raw_stream(dev.index) if stream is None else _stream(stream))
+            rc = f(*args, _raw_stream(index) if stream is None else _stream(stream))
     else:
         rc = f(*args, _stream(stream))
     if rc:
