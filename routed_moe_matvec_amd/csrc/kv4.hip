@@ -14,7 +14,7 @@
 // piece of the page.  Measured: 107 k positions of 8 heads of 128 read back to
 // bf16 in 107 us (5.1 TB/s; a copy reaches 6.2), where four lanes with one
 // position each took 120 and had half again as many loads; 39 k appended from
-// bf16 in 40 us (4.0 TB/s, 27 of them for the reads alone; 34 when the rows are
+// bf16 in 38 us (4.2 TB/s, 27 of them for the reads alone; 34 when the rows are
 // still cached), and 46 with the codes found by comparisons instead of the
 // conversion instruction, bound by them.  Non-temporal reads and writes of the
 // rows would take 9 and 6 us off these, but the prompt attention that reads the
