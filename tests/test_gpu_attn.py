@@ -444,6 +444,66 @@ def test_far_offsets(qg):
     assert int(st) == 0 and int(st2) == 0
 
 
+def test_far_rows(qg):
+    """Rows of k, v and q whose bytes begin past 32-bit offsets."""
+    progress("far rows")
+    n, Hkv, Dh, ld = 300, 2, 64, 1 << 23
+    wide = torch.empty(n, ld, dtype=torch.float16, device="cuda")  # 4.7 GiB
+    k, v, q = (wide[:, i * 512:i * 512 + 128].unflatten(1, (2, 64)) for i in range(3))
+    for i, x in enumerate((k, v, q)):
+        x.copy_(normal(30 + i, (n, Hkv, Dh), torch.float16))
+    c = ah.Cache([n], Hkv, Dh, 64, 33)
+    cache, cu, lens, st = c.device(), ah.cumulative([n]), c.lens_device(), status()
+    qg.kv4_append(1, k, ld, v, ld, n, cu, lens, 1, Hkv, Dh, *cache, st)
+    c.k, c.v = ([ah.values(*ah.quantize(x.double().cpu().numpy()))] for x in (k, v))
+    y, st2 = decode(qg, c, q[n - 3:], 1, 3, Hkv, 0.1, 0, ldq=ld, cache=cache)
+    check_decode(y, c, q[n - 3:].contiguous(), 3, 0.1, 0)
+    y, st3 = prefill(qg, q, k, v, [n], [n], 1, Hkv, Hkv, Dh, 0.1, 0)
+    check_prefill(y, q.contiguous(), k.contiguous(), v.contiguous(), [n], [n], 0.1, 0)
+    qg.kv4_gather(1, k, ld, v, ld, n, cu, lens, 1, Hkv, Dh, *cache, st)
+    assert np.array_equal(k.double().cpu().numpy(), c.k[0]) and np.array_equal(v.double().cpu().numpy(), c.v[0])
+    assert int(st) == int(st2) == int(st3) == 0
+
+
+def test_steps_captured_as_one_graph(qg):
+    """Lengths that grow on the device, the new tokens into the cache and attention over it, captured once: every replay
+    is the next step, and gives what eager calls give."""
+    progress("captured steps")
+    B, H, Hkv, Dh, page, mp, steps = 3, 8, 2, 128, 16, 8, 6
+    start = [0, 14, 61]
+    w, i32 = Hkv * Dh, dict(dtype=torch.int32, device="cuda")
+    pages = torch.randperm(B * mp, generator=torch.Generator().manual_seed(3)).to(torch.int32).cuda().view(B, mp)
+    cu, st = ah.cumulative([1] * B), status()
+    new = [[normal(200 + 3 * s + i, (B, h, Dh), torch.bfloat16) for i, h in enumerate((H, Hkv, Hkv))] for s in range(steps)]
+    q, k, v = (torch.empty_like(x) for x in new[0])
+    nb = qg.attn_decode_workspace_bytes(B, 1, H, Hkv, Dh, mp * page, 0)
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+
+    def state():
+        return (torch.tensor(start, **i32), torch.zeros(B * mp, ah.page_bytes(page, Hkv, Dh), dtype=torch.uint8, device="cuda"),
+                torch.empty(B, H, Dh, device="cuda"))
+
+    def step(lens, kv, y):
+        lens.add_(1)
+        qg.kv4_append(2, k, w, v, w, B, cu, lens, B, Hkv, Dh, pages, mp, page, B * mp, kv, st)
+        qg.attn_decode_kv4(2, q, H * Dh, lens, B, 1, H, Hkv, Dh, 0.1, 0, mp * page, pages, mp, page, B * mp, kv, y, ws, nb, st)
+
+    eager, captured = state(), state()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        step(*captured)
+    for s in range(steps):
+        for x, given in zip((q, k, v), new[s]):
+            x.copy_(given)
+        graph.replay()
+        step(*eager)
+        torch.cuda.synchronize()
+        for a, b in zip(captured, eager):
+            assert torch.equal(a, b), s
+    assert int(st) == 0 and eager[0].tolist() == [n + steps for n in start]
+
+
 # ---- attention of packed prompts -------------------------------------------------------------------------------
 
 def prefill(qg, q, k, v, lq, lk, type, H, Hkv, Dh, scale, window, first=(0, 0), stream=None):
