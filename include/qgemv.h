@@ -462,8 +462,8 @@ int qgemm_prefill_ws(int fmt, const void *W, int N, int K, const uint16_t *x_bf1
  * positions, 0 .. len-1; the query at position p sees the keys j <= p, and with
  * window > 0 only those with j > p - window (window = 0: all).  For each query
  *   y = sum_j softmax_j(scale * q . k_j) v_j     over the keys it sees,
- * and y = 0 where it sees none.  |scale| < 2^127, and scores
- * must stay inside fp32.
+ * and y = 0 where it sees none.  |scale| < 2^127; q . k, and scale * q . k, must
+ * stay inside fp32, and may be of any size there.
  *
  * q, k and v are rows of packed heads, [tokens, heads, Dh], whose rows may be
  * further apart than heads * Dh: ldq, ldk, ldv count elements from one token

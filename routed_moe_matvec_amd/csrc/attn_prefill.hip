@@ -18,7 +18,9 @@
 // Weights are rounded to the 16-bit type for their product with V, as is
 // y: the two roundings are of one size, and scores, maxima and sums are fp32.
 // fp16 weights are 2^11 times as large, below 2^15: those of a long prompt's
-// many far keys would otherwise be subnormal, or 0.
+// many far keys would otherwise be subnormal, or 0.  The running maximum is one
+// of q . k, not scaled, and is taken off the scores themselves where it is large
+// (SoftmaxBase; 0 to 1.5% of the time).
 //
 // One prompt of 16384 tokens, 32 heads of 128 with 8 key heads, bf16: 2.02 to
 // 2.09 ms, 1053 to 1089 TFLOP/s (a large library product reaches 1219).  The matrix cores are busy
@@ -188,8 +190,10 @@ __device__ __forceinline__ PreWork pre_by_slot(const PrefillArgs &a, int slot) {
     return w;
 }
 
+// 64 channels with the keys split in two: 128 registers, or a compute unit holds
+// three workgroups in place of four.
 template <int TYPE, int DH, int KS>
-__global__ __launch_bounds__(kPreWaves *kWave, DH == 256 || KS == 4 ? 1 : 2) void attn_prefill_kernel(PrefillArgs a) {
+__global__ __launch_bounds__(kPreWaves *kWave, DH == 256 || KS == 4 ? 1 : DH == 64 && KS == 2 ? 4 : 2) void attn_prefill_kernel(PrefillArgs a) {
     typedef typename ElemOf<TYPE>::type T;
     typedef PreElem<TYPE> E;
     typedef PreTile<DH, KS> L;
@@ -246,7 +250,8 @@ __global__ __launch_bounds__(kPreWaves *kWave, DH == 256 || KS == 4 ? 1 : 2) voi
     for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[i][j] = 0.f;
-    float m = -INFINITY, muse = 0.f, l = 0.f;
+    float m = -INFINITY, muse = 0.f, l = 0.f;  // m: largest q . k, not scaled
+    unsigned long long far = 0;                // rows whose maximum is taken off their scores
 
     // A tile's copy: each wave takes every fourth KiB; rows behind the last key repeat it.
     constexpr int RPK = 1024 / (DH * 2), KIB = L::BYTES / 1024;  // rows of a KiB
@@ -323,7 +328,7 @@ __global__ __launch_bounds__(kPreWaves *kWave, DH == 256 || KS == 4 ? 1 : 2) voi
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int j = 0; j < 16; ++j) mt = __builtin_fmaxf(mt, t[n][j]);
-            mt = half_max(mt) * a.scale;
+            mt = half_max(mt);
         }
         if constexpr (do_v.value) {
 #pragma unroll
@@ -341,11 +346,21 @@ __global__ __launch_bounds__(kPreWaves *kWave, DH == 256 || KS == 4 ? 1 : 2) voi
                 }
         }
         if constexpr (do_s.value) {
-            if (__ballot(mt > m + E::kSlack)) {
-                const float mn = __builtin_fmaxf(m, mt), use = mn == -INFINITY ? 0.f : mn;
-                const float keep = __builtin_amdgcn_exp2f(m - use);
+            if (__ballot((mt - m) * a.scale > E::kSlack) | far) {
+                const float mn = __builtin_fmaxf(m, mt);
+                const unsigned long long now = __ballot(softmax_far(mn, a.scale));
+                const float keep = softmax_rebase(m, mn, a.scale, E::kShift, far | now);
                 m = mn;
-                muse = use - E::kShift;
+                far = now;
+                muse = m == -INFINITY ? 0.f : m * a.scale - E::kShift;
+                if (far) {
+                    const SoftmaxBase base = softmax_base(m, a.scale, E::kShift);
+                    muse = base.shifted;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) t[n][j] -= base.raw;
+                }
                 l *= keep;
 #pragma unroll
                 for (int i = 0; i < MT; ++i) o[i] *= keep;
@@ -391,12 +406,17 @@ __global__ __launch_bounds__(kPreWaves *kWave, DH == 256 || KS == 4 ? 1 : 2) voi
         if (hf == 0) sml[ks][rw][c] = f32x2{m, l};
         __syncthreads();
         float top = -INFINITY, sum = 0.f;
+        bool any_far = false;
 #pragma unroll
-        for (int x = 0; x < KS; ++x) top = __builtin_fmaxf(top, sml[x][rw][c][0]);
-        const float use_top = top == -INFINITY ? 0.f : top;
+        for (int x = 0; x < KS; ++x) {
+            top = __builtin_fmaxf(top, sml[x][rw][c][0]);
+            any_far = any_far || softmax_far(sml[x][rw][c][0], a.scale);
+        }
+        any_far = __ballot(any_far);
 #pragma unroll
-        for (int x = 0; x < KS; ++x) sum += sml[x][rw][c][1] * __builtin_amdgcn_exp2f(sml[x][rw][c][0] - use_top);
-        const float keep = __builtin_amdgcn_exp2f(m - use_top);
+        for (int x = 0; x < KS; ++x)
+            sum += sml[x][rw][c][1] * softmax_rebase(sml[x][rw][c][0], top, a.scale, E::kShift, any_far);
+        const float keep = softmax_rebase(m, top, a.scale, E::kShift, any_far);
         l = sum;
         static_assert(L::BYTES >= 32 * DH * 4 && (KS - 1) * L::RW <= 4, "a wave's sums fit one object");
         auto room = [&](int i) { return (f32x4 *)(i == 0 ? sk0 : i == 1 ? sk1 : i == 2 ? sv0 : sv1); };

@@ -109,6 +109,34 @@ __device__ __forceinline__ int wave_find_last(int B, int x, F key) {
     return __builtin_amdgcn_readfirstlane(lo);
 }
 
+// What the softmax weights of a row are relative to, from the largest score m =
+// max q . k so far (-inf: none): a score s has the weight 2^((s - raw) * scale -
+// shifted).  Up to 2^16 (scaled) raw is 0 and shifted the scaled maximum, so that
+// a weight takes one fused multiply-add: the maximum's own rounding moves all
+// weights of the row alike, by at most 2^-8 in the exponent.  A larger one would
+// move them out of range (at 1e10 by 2^440), so there the maximum itself is raw and
+// is taken off the scores first, exactly where it counts.
+struct SoftmaxBase {
+    float raw, shifted;
+};
+__device__ __forceinline__ bool softmax_far(float m, float scale) {
+    return __builtin_fabsf(m * scale) > 65536.f && m > -INFINITY;
+}
+__device__ __forceinline__ SoftmaxBase softmax_base(float m, float scale, float shift) {
+    if (softmax_far(m, scale)) return {m, -shift};
+    return {0.f, m == -INFINITY ? 0.f : m * scale - shift};
+}
+// The factor that takes weights relative to maximum `from` to maximum `to`; `far`,
+// the same in the whole wave, says whether any of them may be far.
+__device__ __forceinline__ float softmax_rebase(float from, float to, float scale, float shift, bool far) {
+    float x = from * scale - shift - (to == -INFINITY ? 0.f : to * scale - shift);
+    if (far) {
+        const SoftmaxBase f = softmax_base(from, scale, shift), t = softmax_base(to, scale, shift);
+        x = from == -INFINITY ? from : __builtin_fmaf(f.raw - t.raw, scale, f.shifted - t.shifted);
+    }
+    return __builtin_amdgcn_exp2f(x);
+}
+
 inline bool kv4_cache_shape_ok(int B, int Hkv, int Dh, int max_pages, int page, int num_pages) {
     return B >= 1 && B <= QG_MAX_SEQS && Hkv >= 1 && Hkv <= QG_MAX_HEADS && (Dh == 64 || Dh == 128 || Dh == 256) &&
            max_pages >= 1 && num_pages >= 1 && page >= 16 && page <= QG_MAX_PAGE && (page & (page - 1)) == 0 &&
