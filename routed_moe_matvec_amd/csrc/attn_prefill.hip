@@ -20,7 +20,7 @@
 // fp16 weights are 2^11 times as large, below 2^15: those of a long prompt's
 // many far keys would otherwise be subnormal, or 0.  The running maximum is one
 // of q . k, not scaled, and is taken off the scores themselves where it is large
-// (SoftmaxBase; 0 to 1.5% of the time).
+// (RunningMax; 0 to 2% of the time, 3 for 512 queries of 16384 keys).
 //
 // One prompt of 16384 tokens, 32 heads of 128 with 8 key heads, bf16: 2.02 to
 // 2.09 ms, 1053 to 1089 TFLOP/s (a large library product reaches 1219).  The matrix cores are busy
@@ -250,8 +250,8 @@ __global__ __launch_bounds__(kPreWaves *kWave, DH == 256 || KS == 4 ? 1 : DH == 
     for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[i][j] = 0.f;
-    float m = -INFINITY, muse = 0.f, l = 0.f;  // m: largest q . k, not scaled
-    unsigned long long far = 0;                // rows whose maximum is taken off their scores
+    RunningMax top;
+    float l = 0.f;
 
     // A tile's copy: each wave takes every fourth KiB; rows behind the last key repeat it.
     constexpr int RPK = 1024 / (DH * 2), KIB = L::BYTES / 1024;  // rows of a KiB
@@ -299,7 +299,7 @@ __global__ __launch_bounds__(kPreWaves *kWave, DH == 256 || KS == 4 ? 1 : DH == 
             for (int n = 0; n < NT; ++n) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    s[n][j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][j], a.scale, -muse));
+                    s[n][j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][j], a.scale, -top.muse));
                     l += s[n][j];
                 }
 #pragma unroll
@@ -346,20 +346,14 @@ __global__ __launch_bounds__(kPreWaves *kWave, DH == 256 || KS == 4 ? 1 : DH == 
                 }
         }
         if constexpr (do_s.value) {
-            if (__ballot((mt - m) * a.scale > E::kSlack) | far) {
-                const float mn = __builtin_fmaxf(m, mt);
-                const unsigned long long now = __ballot(softmax_far(mn, a.scale));
-                const float keep = softmax_rebase(m, mn, a.scale, E::kShift, far | now);
-                m = mn;
-                far = now;
-                muse = m == -INFINITY ? 0.f : m * a.scale - E::kShift;
-                if (far) {
-                    const SoftmaxBase base = softmax_base(m, a.scale, E::kShift);
-                    muse = base.shifted;
+            if (__ballot((mt - top.m) * a.scale > E::kSlack) | top.far) {
+                const float keep = top.raise(mt, a.scale, E::kShift);
+                if (top.far) {
+                    const float raw = top.raw(a.scale);
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) t[n][j] -= base.raw;
+                        for (int j = 0; j < 16; ++j) t[n][j] -= raw;
                 }
                 l *= keep;
 #pragma unroll
@@ -403,20 +397,17 @@ __global__ __launch_bounds__(kPreWaves *kWave, DH == 256 || KS == 4 ? 1 : DH == 
     }
     l += shfl_xor(l, 32);
     if constexpr (KS > 1) {  // join the waves that share queries, through the stages
-        if (hf == 0) sml[ks][rw][c] = f32x2{m, l};
+        const float exact = top.exact(a.scale, E::kShift);
+        if (hf == 0) sml[ks][rw][c] = f32x2{top.m, l * exact};
         __syncthreads();
-        float top = -INFINITY, sum = 0.f;
-        bool any_far = false;
+        float most = -INFINITY, sum = 0.f;
 #pragma unroll
-        for (int x = 0; x < KS; ++x) {
-            top = __builtin_fmaxf(top, sml[x][rw][c][0]);
-            any_far = any_far || softmax_far(sml[x][rw][c][0], a.scale);
-        }
-        any_far = __ballot(any_far);
+        for (int x = 0; x < KS; ++x) most = __builtin_fmaxf(most, sml[x][rw][c][0]);
+        if (most == -INFINITY) most = 0.f;
 #pragma unroll
         for (int x = 0; x < KS; ++x)
-            sum += sml[x][rw][c][1] * softmax_rebase(sml[x][rw][c][0], top, a.scale, E::kShift, any_far);
-        const float keep = softmax_rebase(m, top, a.scale, E::kShift, any_far);
+            sum += sml[x][rw][c][1] * __builtin_amdgcn_exp2f((sml[x][rw][c][0] - most) * a.scale);
+        const float keep = exact * __builtin_amdgcn_exp2f((top.m - most) * a.scale);
         l = sum;
         static_assert(L::BYTES >= 32 * DH * 4 && (KS - 1) * L::RW <= 4, "a wave's sums fit one object");
         auto room = [&](int i) { return (f32x4 *)(i == 0 ? sk0 : i == 1 ? sk1 : i == 2 ? sv0 : sv1); };

@@ -109,33 +109,43 @@ __device__ __forceinline__ int wave_find_last(int B, int x, F key) {
     return __builtin_amdgcn_readfirstlane(lo);
 }
 
-// What the softmax weights of a row are relative to, from the largest score m =
-// max q . k so far (-inf: none): a score s has the weight 2^((s - raw) * scale -
-// shifted).  Up to 2^16 (scaled) raw is 0 and shifted the scaled maximum, so that
-// a weight takes one fused multiply-add: the maximum's own rounding moves all
-// weights of the row alike, by at most 2^-8 in the exponent.  A larger one would
-// move them out of range (at 1e10 by 2^440), so there the maximum itself is raw and
-// is taken off the scores first, exactly where it counts.
-struct SoftmaxBase {
-    float raw, shifted;
-};
-__device__ __forceinline__ bool softmax_far(float m, float scale) {
-    return __builtin_fabsf(m * scale) > 65536.f && m > -INFINITY;
-}
-__device__ __forceinline__ SoftmaxBase softmax_base(float m, float scale, float shift) {
-    if (softmax_far(m, scale)) return {m, -shift};
-    return {0.f, m == -INFINITY ? 0.f : m * scale - shift};
-}
-// The factor that takes weights relative to maximum `from` to maximum `to`; `far`,
-// the same in the whole wave, says whether any of them may be far.
-__device__ __forceinline__ float softmax_rebase(float from, float to, float scale, float shift, bool far) {
-    float x = from * scale - shift - (to == -INFINITY ? 0.f : to * scale - shift);
-    if (far) {
-        const SoftmaxBase f = softmax_base(from, scale, shift), t = softmax_base(to, scale, shift);
-        x = from == -INFINITY ? from : __builtin_fmaf(f.raw - t.raw, scale, f.shifted - t.shifted);
+// The running maximum of a softmax, of scores q . k that are not scaled yet.  A
+// score s has the weight 2^((s - raw) * scale - muse).  Up to 2^16 (scaled) raw is 0
+// and muse the scaled maximum less `shift`, so that a weight takes one fused
+// multiply-add: the maximum's own rounding moves all weights of the row alike, by
+// at most 2^-8 in the exponent.  A larger maximum would move them out of range (at
+// 1e10 by 2^440): it is raw itself, taken off the scores first (far rows).
+struct RunningMax {
+    float m = -INFINITY, muse = 0.f;
+    unsigned long long far = 0;  // the lanes of the wave whose rows are far
+
+    __device__ __forceinline__ bool is_far(float x, float scale) const {
+        return __builtin_fabsf(x * scale) > 65536.f && x > -INFINITY;
     }
-    return __builtin_amdgcn_exp2f(x);
-}
+    // To the maximum with mt; returns the factor that this means for the row's sums.
+    __device__ __forceinline__ float raise(float mt, float scale, float shift) {
+        const float mn = __builtin_fmaxf(m, mt);
+        float to = mn == -INFINITY ? 0.f : mn * scale - shift, e = m * scale - shift - to;
+        const unsigned long long now = __ballot(is_far(mn, scale));
+        if (far | now) {
+            const float from_raw = is_far(m, scale) ? m : 0.f, to_raw = is_far(mn, scale) ? mn : 0.f;
+            if (to_raw != 0.f) to = -shift;
+            e = m == -INFINITY ? m : __builtin_fmaf(from_raw - to_raw, scale, muse - to);
+            far = now;
+        }
+        m = mn;
+        muse = to;
+        return __builtin_amdgcn_exp2f(e);
+    }
+    // What is to be taken off the scores (far != 0).
+    __device__ __forceinline__ float raw(float scale) const { return is_far(m, scale) ? m : 0.f; }
+    // The factor that makes the row's sums relative to m * scale - shift exactly, so that
+    // rows are joined by the difference of their maxima (0 where nothing was seen).
+    __device__ __forceinline__ float exact(float scale, float shift) const {
+        const float at = far && is_far(m, scale) ? 0.f : m;
+        return m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(shift - __builtin_fmaf(at, scale, -muse));
+    }
+};
 
 inline bool kv4_cache_shape_ok(int B, int Hkv, int Dh, int max_pages, int page, int num_pages) {
     return B >= 1 && B <= QG_MAX_SEQS && Hkv >= 1 && Hkv <= QG_MAX_HEADS && (Dh == 64 || Dh == 128 || Dh == 256) &&
