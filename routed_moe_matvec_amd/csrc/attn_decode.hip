@@ -14,7 +14,9 @@
 // hardware conversion takes the UE8M0 scale along), fp32 queries go in as
 // three bf16 parts (24 bits, exact) and fp16 ones as two, weights as three
 // (with two the result was off by 2.4e-6 of its norm, ten times as much as with
-// three).  Products and sums are fp32.
+// three).  Products and sums are fp32.  The running maximum is one of q . k, not
+// scaled, and is taken off the scores themselves where it is large (RunningMax; 0
+// to 3% of the time).
 #include <type_traits>
 
 #include "common.h"
@@ -70,7 +72,7 @@ struct DecodeArgs {
     const void *q;
     float *y;
     float *po;   // [B, H * Tq, chunks, Dh] partial sums
-    f32x2 *pml;  // [B, H * Tq, chunks] maximum (base 2) and sum
+    f32x2 *pml;  // [B, H * Tq, chunks] largest q . k and sum
     int ldq, Tq, H, G, window, max_len, chunks;
     float scale;  // times log2(e), not negative
     float qsign;  // 1, -1 (a negative scale) or 0 (scale 0)
@@ -286,6 +288,7 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
     const int page = 1 << a.c.page_log2;
     const int pos = len - a.Tq + t;                       // this row's position
     const int see_hi = live ? pos + 1 : 0, see_lo = a.window ? max(pos - a.window + 1, 0) : 0;
+    const uint32_t seen_here = (uint32_t)max(min(see_hi, last) - see_lo, 0);  // positions from see_lo on
     const int seen = a.window ? len - a.Tq - a.window + 1 : 0;  // the first position that a row sees
     const size_t region = kv4_region_bytes(page, DH);
     const DecLane<DH> ln(lane);
@@ -352,7 +355,8 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
     f32x4 o[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    float m = -INFINITY, muse = 0.f, l = 0.f;
+    RunningMax most;
+    float l = 0.f;
 
     // A step's keys are loaded again as soon as its scores are there, its
     // values when they are summed: the loads of the next step run beside the
@@ -393,7 +397,7 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
         if (!whole) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const uint32_t span = cur_ok[x] ? (uint32_t)max(min(see_hi, last) - see_lo, 0) : 0u;
+                const uint32_t span = cur_ok[x] ? seen_here : 0u;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if ((uint32_t)(j + 16 * x + 4 * g + i - see_lo) >= span) s[x][i] = -INFINITY;
@@ -402,12 +406,14 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
         float mt = s[0][0];
 #pragma unroll
         for (int i = 1; i < 8; ++i) mt = __builtin_fmaxf(mt, s[i / 4][i % 4]);
-        mt = row_max(mt) * a.scale;  // in powers of two, as m
-        if (__ballot(mt > m + kDecSlack)) {
-            const float mn = __builtin_fmaxf(m, mt);
-            muse = mn == -INFINITY ? 0.f : mn;
-            const float keep = __builtin_amdgcn_exp2f(m - muse);
-            m = mn;
+        mt = row_max(mt);
+        if (__ballot((mt - most.m) * a.scale > kDecSlack) | most.far) {
+            const float keep = most.raise(mt, a.scale, 0.f);
+            if (most.far) {
+                const float raw = most.raw(a.scale);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s[i / 4][i % 4] -= raw;
+            }
             l *= keep;
 #pragma unroll
             for (int i = 0; i < MT; ++i) o[i] *= keep;
@@ -417,7 +423,7 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
             float p[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i / 4][i % 4], a.scale, -muse));
+                p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i / 4][i % 4], a.scale, -most.muse));
                 l += p[i];
             }
 #pragma unroll
@@ -490,8 +496,9 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
     // join the waves: maxima first, then the sums of PER channel tiles at a
     // time through LDS, added and written by all threads (one wave writing
     // alone cost 22 of 117 us with 16 rows of 256 channels a workgroup)
-    l = row_sum(l);
-    if (g == 0) sml[wave][c] = f32x2{m, l};
+    const float exact = most.exact(a.scale, 0.f);
+    l = row_sum(l) * exact;
+    if (g == 0) sml[wave][c] = f32x2{most.m, l};
     __syncthreads();  // and every wave is done with the queries
     auto joined = [&](int r) {  // maximum and sum of a row
         float top = -INFINITY, sum = 0.f;
@@ -499,10 +506,11 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
         for (int w = 0; w < kDecWaves; ++w) top = __builtin_fmaxf(top, sml[w][r][0]);
 #pragma unroll
         for (int w = 0; w < kDecWaves; ++w)
-            sum += sml[w][r][1] * __builtin_amdgcn_exp2f(sml[w][r][0] - (top == -INFINITY ? 0.f : top));
+            sum += sml[w][r][1] * __builtin_amdgcn_exp2f((sml[w][r][0] - (top == -INFINITY ? 0.f : top)) * a.scale);
         return f32x2{top, sum};
     };
-    const float top = joined(c)[0], keep = __builtin_amdgcn_exp2f(m - (top == -INFINITY ? 0.f : top));
+    const float top = joined(c)[0];
+    const float keep = exact * __builtin_amdgcn_exp2f((most.m - (top == -INFINITY ? 0.f : top)) * a.scale);
     // o[8 y + i][k]: channel ((16 y + 4 g + k) * 8 + i), or (4 g + k) * 4 + i for 64 channels
     // what this thread adds and writes: a row's PART tiles from tile wi on, register wk of lane group wg
     constexpr int PART = PER / SLOTS;
@@ -581,7 +589,7 @@ __global__ __launch_bounds__(256) void attn_decode_join_kernel(DecodeArgs a) {
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
     auto add = [&](int i, f32x4 o) {
         const f32x2 ml = a.pml[at + i];
-        const float w = __builtin_amdgcn_exp2f(ml[0] - use);
+        const float w = __builtin_amdgcn_exp2f((ml[0] - use) * a.scale);
         l += ml[1] * w;
         acc += o * w;
     };

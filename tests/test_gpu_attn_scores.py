@@ -6,7 +6,7 @@ import torch
 
 from tests import attn_helpers as ah
 from tests.gpu_util import progress
-from tests.test_gpu_attn import normal, prefill
+from tests.test_gpu_attn import decode, normal, prefill
 
 pytestmark = pytest.mark.gpu
 
@@ -25,12 +25,17 @@ def qg():
 
 def prefill_limit(ref, a, dtype):
     """y is rounded once, u of it; a weight is rounded to the type, u of it and of its part of sum p |v|; fp32 sums and
-    exponentials, less than 2^-16: with exact q . k, a weight's exponent is off by the roundings of scale, of log2(e), of
-    their product and of the difference, each 2^-24 of it; below -26 (base 2) a weight no longer counts in fp32.  So it is off
-    by 26 * 4 * 2^-24 of ln 2 of itself and the exponential's own 2^-22; twice, in the sum and in what divides it; and the
-    sums, a few hundred additions of 2^-24.  310 weights under fp16's least, 2^-36 of the largest, with |v| < 6 are under 2^-25."""
+    exponentials as below, 2^-16; 310 weights under fp16's least, 2^-36 of the largest, with |v| < 6 are under 2^-25."""
     u = torch.finfo(dtype).eps / 2
     return u * ref.abs() + (u + 2.0**-16) * (1 + u) * a + (2.0**-25 if dtype == torch.float16 else 0.0)
+
+
+def decode_limit(a):
+    """With exact q . k, a weight's exponent is off by the roundings of scale, of log2(e), of their product and of the
+    difference, each 2^-24 of it; below -26 (base 2) a weight no longer counts in fp32.  So it is off by 26 * 4 * 2^-24 of
+    ln 2 of itself and the exponential's own 2^-22; twice, in the sum and in what divides it; and the sums, a few hundred
+    additions of 2^-24: less than 2^-16."""
+    return 2.0**-16 * a + 1e-37
 
 
 @pytest.mark.parametrize("type", [1, 2])
@@ -100,3 +105,75 @@ def test_prefill_far_and_near_rows(qg, order, H, B, type):
             ref, a, _ = ah.attend(q[at, :1].double(), k[at].double(), v[at].double(), 64.0 * up, window)
             err = (y[at].double() - ref).abs()
             assert bool((err <= prefill_limit(ref, a, dt)).all()), (Dh, b, float(err.nan_to_num(9e9).max()))
+
+
+def cache_with_keys(c, keys):
+    """Cache c with keys [positions, Dh] (E2M1 values, scale 1) for every sequence and head, in place of its own."""
+    for b, n in enumerate(c.lens):
+        x = np.broadcast_to(keys[:n, None], (n, c.Hkv, c.Dh))
+        scales = np.full((n, c.Hkv, c.Dh // 32), 127, np.uint8)
+        codes = np.searchsorted(ah.E2M1[:8], np.abs(x)).astype(np.uint8) | np.signbit(x).astype(np.uint8) << 3
+        c.put(b, 0, codes, scales, np.arange(n))
+        c.k[b] = ah.values(codes, scales)
+        assert np.array_equal(c.k[b], x)
+    return c
+
+
+@pytest.mark.parametrize("type", [0, 1, 2])
+@pytest.mark.parametrize("score", SCORES)
+def test_decode_one_and_equal_keys(qg, score, type):
+    progress("decode equal scores %g type %d" % (score, type))
+    lens = [1, 40, 700, 5000]
+    for Dh, G, Tq in ((64, 1, 1), (128, 4, 2), (256, 16, 1)):
+        c = ah.Cache(lens, 2, Dh, 16, 21).fill(22)
+        cache_with_keys(c, np.full((max(lens), Dh), 4.0))
+        q = torch.full((len(lens) * Tq, 2 * G, Dh), 4.0, dtype=ah.TYPES[type], device="cuda")
+        for window in (1, 0):
+            for sign in (1.0, -1.0):
+                y, st = decode(qg, c, q, type, Tq, 2 * G, sign * score / (16 * Dh), window)
+                assert int(st) == 0
+                for b, n in enumerate(lens):
+                    at = slice(b * Tq, (b + 1) * Tq)
+                    k, v = (torch.from_numpy(x[b]).cuda() for x in (c.k, c.v))
+                    ref, a, _ = ah.attend(q[at].double(), k, v, 0.0, window)  # equal scores
+                    err = (y[at].double() - ref).abs()
+                    assert bool((err <= decode_limit(a)).all()), (Dh, window, sign, n, float(err.nan_to_num(9e9).max()))
+
+
+@pytest.mark.parametrize("type", [0, 1, 2])
+@pytest.mark.parametrize("order", ["any", "rising", "falling"])
+def test_decode_far_and_near_rows(qg, order, type):
+    """As for prompts; several chunks and the join among them."""
+    progress("decode scores of all sizes %s type %d" % (order, type))
+    lens = [33, 640, 2500, 9001]
+    for Dh, G, Tq, window in ((64, 31, 1, 0), (128, 8, 1, 0), (128, 16, 2, 1700), (256, 5, 7, 0)):
+        q, k = exact_scores(G * Tq, max(lens), Dh, order, 5)
+        c = ah.Cache(lens, 1, Dh, 32, 23).fill(24)
+        cache_with_keys(c, k[:, 0].cpu().numpy())
+        up = 2.0**10 if type == 1 else 1.0
+        q = (q / up).to(ah.TYPES[type]).view(Tq, G, Dh).repeat(len(lens), 1, 1)
+        y, st = decode(qg, c, q, type, Tq, G, 64.0 * up, window)
+        assert int(st) == 0
+        for b, n in enumerate(lens):
+            at = slice(b * Tq, (b + 1) * Tq)
+            kk, vv = (torch.from_numpy(x[b]).cuda() for x in (c.k, c.v))
+            ref, a, _ = ah.attend(q[at].double(), kk, vv, 64.0 * up, window)
+            err = (y[at].double() - ref).abs()
+            assert bool((err <= decode_limit(a)).all()), (Dh, G, Tq, n, float(err.nan_to_num(9e9).max()))
+
+
+def test_decode_products_of_real_numbers(qg):
+    """fp32 queries of about 1e10 in every channel: one visible key, and one key above all others."""
+    progress("decode products of 1e10")
+    for Dh in (64, 128, 256):
+        c = ah.Cache([1, 700], 1, Dh, 16, 25).fill(26)
+        q = normal(27, (2, 4, Dh), torch.float32, 1e10)
+        y, _ = decode(qg, c, q, 0, 1, 4, 1.0, 0)
+        for b in range(2):
+            k, v = (torch.from_numpy(x[b]).cuda() for x in (c.k, c.v))
+            s = torch.matmul(q[b].double(), k[:, 0].t().contiguous())
+            best = s.topk(min(2, s.shape[1]), dim=1)
+            if s.shape[1] > 1:  # more apart than the scores' own roundings
+                assert float((best.values[:, 0] - best.values[:, 1]).min()) > 1e6
+            ref = v[best.indices[:, 0], 0]
+            assert bool(((y[b].double() - ref).abs() <= decode_limit(ref.abs())).all()), (Dh, b)
