@@ -90,15 +90,17 @@ __device__ __forceinline__ int dec_range(const DecodeArgs &a, int b, int *len, i
     return n - *begin;
 }
 
-// 8 elements of q as PARTS bf16 vectors whose sum they are.
+// 8 elements of q as PARTS bf16 vectors whose sum they are.  The first part of
+// fp32's largest numbers is bf16's largest, not Inf.
 template <int PARTS, class T>
 __device__ __forceinline__ void split8(const Raw8<T> &r, float sign, bf16x8 (&out)[PARTS]) {
+    constexpr float kMost = 0x1.fep127f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         float x = elem(r, i) * sign;
 #pragma unroll
         for (int s = 0; s < PARTS; ++s) {
-            const bf16_t h = (bf16_t)x;
+            const bf16_t h = (bf16_t)(PARTS == 3 && s == 0 ? __builtin_amdgcn_fmed3f(x, -kMost, kMost) : x);
             out[s][i] = h;
             x -= (float)h;
         }

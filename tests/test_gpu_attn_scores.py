@@ -177,3 +177,25 @@ def test_decode_products_of_real_numbers(qg):
                 assert float((best.values[:, 0] - best.values[:, 1]).min()) > 1e6
             ref = v[best.indices[:, 0], 0]
             assert bool(((y[b].double() - ref).abs() <= decode_limit(ref.abs())).all()), (Dh, b)
+
+
+@pytest.mark.parametrize("Dh,G", [(64, 1), (128, 8), (256, 16)])
+def test_decode_largest_queries(qg, Dh, G):
+    """fp32 queries up to the largest finite value, at the keys of the least scales; each score is moderate.  The limit is
+    attn_helpers' own."""
+    progress("decode queries of 3.4e38, Dh %d G %d" % (Dh, G))
+    c = ah.Cache([300, 40], 1, Dh, 16, 31).fill(32, 7, 8)
+    for b, n in enumerate(c.lens):  # values of ordinary size
+        codes = np.random.default_rng(b).integers(0, 16, (n, 1, Dh)).astype(np.uint8)
+        scales = np.full((n, 1, Dh // 32), 126, np.uint8)
+        c.put(b, 1, codes, scales, np.arange(n))
+        c.v[b] = ah.values(codes, scales)
+    q = normal(34, (2, G, Dh), torch.float32, 1e37)
+    top = torch.finfo(torch.float32).max
+    q[:, :, 0], q[:, :, 1], q[:, 0, 2] = top, -top, torch.nextafter(torch.tensor(top), torch.tensor(0.0)).item()
+    y, st = decode(qg, c, q, 0, 1, G, 0.01, 0)
+    assert int(st) == 0
+    for b, n in enumerate(c.lens):
+        k, v = (torch.from_numpy(x[b]).cuda() for x in (c.k, c.v))
+        ref, a, big = ah.attend(q[b:b + 1].double(), k, v, 0.01, 0)
+        assert bool(((y[b:b + 1].double() - ref).abs() <= ah.decode_tolerance(a, big, n, Dh)).all()), b
