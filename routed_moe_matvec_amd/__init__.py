@@ -277,12 +277,25 @@ else:
     _TYPES, _I32, _FP32 = {}, None, None
 
 
-def _rows_ptr(t, name: str, type: int, rows: int, width: int, ld: int):
+def _device_of(first):
+    """Device index of the call's first tensor, which every other has to share (None: an address)."""
+    return first.get_device() if isinstance(first, _Tensor) else None
+
+
+def _elsewhere(t, name: str, at: int, device):
+    if at < 0:
+        raise TypeError("libqgemv takes device tensors; got %s on %s" % (name, t.device))
+    if device is not None:
+        raise ValueError("%s is on device %d, the call's first tensor on device %d" % (name, at, device))
+
+
+def _rows_ptr(t, name: str, device, type: int, rows: int, width: int, ld: int):
     """Device pointer of `rows` rows of `width` elements, `ld` elements apart."""
     if not isinstance(t, _Tensor):
         return _ptr(t)
-    if not t.is_cuda:
-        raise TypeError("libqgemv takes device tensors; got %s on %s" % (name, t.device))
+    at = t.get_device()
+    if at != device or at < 0:
+        _elsewhere(t, name, at, device)
     if t.dtype is not _TYPES.get(type, t.dtype):
         raise TypeError("%s is %s, the call's type is %s" % (name, t.dtype, _TYPES[type]))
     have = t.numel()
@@ -301,10 +314,13 @@ def _rows_ptr(t, name: str, type: int, rows: int, width: int, ld: int):
     return t.data_ptr()
 
 
-def _array_ptr(t, name: str, dtype, count: int):
+def _array_ptr(t, name: str, device, dtype, count: int):
     """Device pointer of a dense tensor that holds `count` values of dtype (None: any type, counted in bytes)."""
     if not isinstance(t, _Tensor):
         return _ptr(t)
+    at = t.get_device()
+    if at != device or at < 0:
+        _elsewhere(t, name, at, device)
     have = t.numel()
     if dtype is None:
         have *= t.element_size()
@@ -312,13 +328,12 @@ def _array_ptr(t, name: str, dtype, count: int):
         raise TypeError("%s is %s, not %s" % (name, t.dtype, dtype))
     if have < count:
         raise ValueError("%s holds %d, the call needs %d" % (name, have, count))
-    return t.data_ptr() if t.is_cuda and t.is_contiguous() else _ptr(t)
+    return t.data_ptr() if t.is_contiguous() else _ptr(t)
 
 
-def _call_on(what: str, f, first, args, stream):
-    """f(*args, stream) with the device of tensor `first` current, as its launch needs."""
-    if isinstance(first, _Tensor):
-        index = first.get_device()
+def _call_on(what: str, f, first, index, args, stream):
+    """f(*args, stream) with the device `index` of tensor `first` current, as its launch needs."""
+    if index is not None:
         if index != _cur_device():
             with torch.cuda.device(index):
                 rc = f(*args, _stream(stream, first))
@@ -330,10 +345,10 @@ def _call_on(what: str, f, first, args, stream):
         raise QGError(rc, what)
 
 
-def _cache_args(pages, B: int, max_pages: int, page: int, num_pages: int, Hkv: int, Dh: int, kv):
+def _cache_args(dev, pages, B: int, max_pages: int, page: int, num_pages: int, Hkv: int, Dh: int, kv):
     each = Hkv * page * Dh // 16 * 17 if page & (page - 1) == 0 else 0  # other sizes are the library's to refuse
-    return (_array_ptr(pages, "pages", _I32, B * max_pages), max_pages, page, num_pages,
-            _array_ptr(kv, "kv", None, num_pages * each))
+    return (_array_ptr(pages, "pages", dev, _I32, B * max_pages), max_pages, page, num_pages,
+            _array_ptr(kv, "kv", dev, None, num_pages * each))
 
 
 def kv4_page_bytes(page: int, Hkv: int, Dh: int) -> int:
@@ -342,11 +357,12 @@ def kv4_page_bytes(page: int, Hkv: int, Dh: int) -> int:
 
 def _kv4(what, f, type, k, ldk, v, ldv, n, cu, lens, B, Hkv, Dh, pages, max_pages, page, num_pages, kv, d_status,
          stream):
-    w = Hkv * Dh
-    _call_on(what, f, k, (type, _rows_ptr(k, "k", type, n, w, ldk), ldk, _rows_ptr(v, "v", type, n, w, ldv), ldv, n,
-                          _array_ptr(cu, "cu", _I32, B + 1), _array_ptr(lens, "lens", _I32, B), B, Hkv, Dh,
-                          *_cache_args(pages, B, max_pages, page, num_pages, Hkv, Dh, kv),
-                          _array_ptr(d_status, "d_status", _I32, 1)), stream)
+    w, dev = Hkv * Dh, _device_of(k)
+    _call_on(what, f, k, dev,
+             (type, _rows_ptr(k, "k", dev, type, n, w, ldk), ldk, _rows_ptr(v, "v", dev, type, n, w, ldv), ldv, n,
+              _array_ptr(cu, "cu", dev, _I32, B + 1), _array_ptr(lens, "lens", dev, _I32, B), B, Hkv, Dh,
+              *_cache_args(dev, pages, B, max_pages, page, num_pages, Hkv, Dh, kv),
+              _array_ptr(d_status, "d_status", dev, _I32, 1)), stream)
 
 
 def kv4_append(type: int, k, ldk: int, v, ldv: int, n: int, cu, lens, B: int, Hkv: int, Dh: int, pages,
@@ -368,18 +384,19 @@ def attn_decode_workspace_bytes(B: int, Tq: int, H: int, Hkv: int, Dh: int, max_
 def attn_decode_kv4(type: int, q, ldq: int, lens, B: int, Tq: int, H: int, Hkv: int, Dh: int, scale: float,
                     window: int, max_len: int, pages, max_pages: int, page: int, num_pages: int, kv, y, ws,
                     ws_bytes: int, d_status, stream=None) -> None:
-    _call_on("attn_decode_kv4", _c_decode, q,
-             (type, _rows_ptr(q, "q", type, B * Tq, H * Dh, ldq), ldq, _array_ptr(lens, "lens", _I32, B), B, Tq, H,
-              Hkv, Dh, scale, window, max_len, *_cache_args(pages, B, max_pages, page, num_pages, Hkv, Dh, kv),
-              _array_ptr(y, "y", _FP32, B * Tq * H * Dh), _array_ptr(ws, "ws", None, ws_bytes), ws_bytes,
-              _array_ptr(d_status, "d_status", _I32, 1)), stream)
+    dev = _device_of(q)
+    _call_on("attn_decode_kv4", _c_decode, q, dev,
+             (type, _rows_ptr(q, "q", dev, type, B * Tq, H * Dh, ldq), ldq, _array_ptr(lens, "lens", dev, _I32, B), B,
+              Tq, H, Hkv, Dh, scale, window, max_len, *_cache_args(dev, pages, B, max_pages, page, num_pages, Hkv, Dh, kv),
+              _array_ptr(y, "y", dev, _FP32, B * Tq * H * Dh), _array_ptr(ws, "ws", dev, None, ws_bytes), ws_bytes,
+              _array_ptr(d_status, "d_status", dev, _I32, 1)), stream)
 
 
 def attn_prefill(type: int, q, ldq: int, k, ldk: int, v, ldv: int, nq: int, nk: int, cu_q, cu_k, B: int, H: int,
                  Hkv: int, Dh: int, scale: float, window: int, y, d_status, stream=None) -> None:
-    w = Hkv * Dh
-    _call_on("attn_prefill", _c_attn_prefill, q,
-             (type, _rows_ptr(q, "q", type, nq, H * Dh, ldq), ldq, _rows_ptr(k, "k", type, nk, w, ldk), ldk,
-              _rows_ptr(v, "v", type, nk, w, ldv), ldv, nq, nk, _array_ptr(cu_q, "cu_q", _I32, B + 1),
-              _array_ptr(cu_k, "cu_k", _I32, B + 1), B, H, Hkv, Dh, scale, window,
-              _rows_ptr(y, "y", type, nq, H * Dh, H * Dh), _array_ptr(d_status, "d_status", _I32, 1)), stream)
+    w, dev = Hkv * Dh, _device_of(q)
+    _call_on("attn_prefill", _c_attn_prefill, q, dev,
+             (type, _rows_ptr(q, "q", dev, type, nq, H * Dh, ldq), ldq, _rows_ptr(k, "k", dev, type, nk, w, ldk), ldk,
+              _rows_ptr(v, "v", dev, type, nk, w, ldv), ldv, nq, nk, _array_ptr(cu_q, "cu_q", dev, _I32, B + 1),
+              _array_ptr(cu_k, "cu_k", dev, _I32, B + 1), B, H, Hkv, Dh, scale, window,
+              _rows_ptr(y, "y", dev, type, nq, H * Dh, H * Dh), _array_ptr(d_status, "d_status", dev, _I32, 1)), stream)
