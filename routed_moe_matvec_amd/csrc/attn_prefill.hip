@@ -459,9 +459,13 @@ static int launch_prefill_ks(PrefillArgs a, hipStream_t stream) {
 // those leave compute units without work, 32 queries and split the keys: smaller
 // tiles also spread the triangle of a prompt more evenly.  32 heads of 128, us with
 // 128, 64, 32 queries: 512 of 16384 keys 303, 231; 3 and 20 of 8000 keys 149, -, 87;
-// prompts of 1024 tokens 28.6, 23.9; 2048 (one round exactly) 56, 57; 3000 94, 106; 16384
-// 2076, 2850; of 768 -, 19, 30.  32 heads of 64: 2048 tokens 36.0, 32.5; 16 heads of
-// 256: 2048 tokens 79, 66; 2500 93, 102.
+// prompts of 1024 tokens 28.6, 23.9; 3000 94, 106; 16384 2076, 2850; of 768 -, 19, 30.
+// 32 heads of 64: 2048 tokens 36.0, 32.5; 16 heads of 256: 2048 tokens 79, 66; 2500 93,
+// 102.  One round exactly is the border: tiles of one length are even as they are, a
+// prompt's are not.  128 channels, us with 128, 64 queries: 2048 of 16384 keys 500,
+// 561; 2048 tokens 52.5, 52.2, with a window of 600 34.3, 35.7; 8192 of 8 heads 180,
+// 166: tiles of 128.  64 channels: 311, 331; 34.8, 30.9; 22.9, 19.6; 114, 100, and 256:
+// 562, 646; 78, 64; 42, 51; 273, 198: prompts gain more than the others lose.
 template <int TYPE, int DH>
 static int launch_prefill_dh(const PrefillArgs &a, hipStream_t stream) {
     const long long cus = device_cu_count(), round = DH == 256 ? cus : 2 * cus;
