@@ -473,9 +473,14 @@ int qgemm_prefill_ws(int fmt, const void *W, int N, int K, const uint16_t *x_bf1
  * alignment.  Keys and values that any query of the call sees must be finite;
  * what lies elsewhere (rows of other sequences, positions behind a sequence or
  * before every query's window, unused pages) may hold anything and has no
- * influence.  Outputs and workspaces overlap no input.  One launch holds fewer
- * than 2^24 workgroups: beyond B * Hkv or B * H of some millions a call is
- * refused as QG_ERR_SHAPE.
+ * influence.  A weight reaches 2^8 before the sums are rescaled: max |v| times the
+ * number of keys that a query sees must stay below 2^119.  Outputs and workspaces
+ * overlap no input.  One launch holds fewer than 2^24 workgroups, and a call that
+ * needs more is refused as QG_ERR_SHAPE: attn_prefill from (nq / 128 + B) * H = 2^24
+ * on; the cache moves from (n / 4 + 2 B + 1) * ceil(Hkv * Dh / 512) = 2^26 - 3 on;
+ * attn_decode_kv4 from B * H * Tq = 2^24 on, and from B * Hkv * ceil(H / Hkv * Tq /
+ * 16) times the chunks of a sequence = 2^24 on (its workspace holds B * Tq * H *
+ * (Dh + 2) floats a chunk, or there is one).
  *
  * The cache.  Keys and values are held in pages of `page` positions (a power
  * of two, 16 .. QG_MAX_PAGE) of one sequence: `kv` is num_pages pages of

@@ -1,5 +1,7 @@
 """The binding of the cache and attention calls, without a GPU: tensors of two devices are refused before any launch, whose kernels
 would otherwise read one device's addresses on the other."""
+import ctypes
+
 import pytest
 import torch
 
@@ -60,3 +62,21 @@ def test_tensors_of_two_devices_are_refused(which):
         call = [c for _, c in calls(lambda name: -1 if name == odd else 0)][which]
         with pytest.raises(TypeError):
             call()
+
+
+def test_launches_too_large_for_their_tokens_are_refused():
+    """2^24 workgroups and more from the tokens, not from the sequences; a call below is refused for another reason."""
+    from tests.test_attn_host import AT, DECODE, DECODE_T, MOVE, MOVE_T, PREFILL, PREFILL_T, _call
+    lib = ctypes.CDLL(qg.library_path())
+    long = dict(n=1 << 24, Dh=256, B=1)
+    for name in ("kv4_append", "kv4_gather"):
+        for Hkv, code in ((32, -2), (28, -3)):  # 16 and 14 pieces of a row; the cache 8 bytes off
+            assert _call(lib, name, MOVE_T, {**MOVE, **long, "Hkv": Hkv,
+                                              "ldk": 256 * Hkv, "ldv": 256 * Hkv, "kv": AT + 8}) == code
+    assert _call(lib, "attn_prefill", PREFILL_T, {**PREFILL, "nq": 1 << 24, "nk": 1 << 24, "B": 1, "H": 128, "ldq": 1 << 14}) == -2
+    rows = dict(B=65535, H=512, Hkv=2, ldq=1 << 16, max_len=128)
+    assert _call(lib, "attn_decode_kv4", DECODE_T, {**DECODE, **rows, "ws_bytes": 1 << 62}) == -2
+    chunks = dict(B=2048, H=8, Hkv=8, ldq=1 << 10, max_len=1 << 22, page=65536, max_pages=64)
+    nb = qg.attn_decode_workspace_bytes(2048, 1, 8, 8, 128, 1 << 22, 0)
+    assert nb == 2048 * 8 * 130 * 4 * 1024  # 1024 chunks: 2^24 workgroups
+    assert _call(lib, "attn_decode_kv4", DECODE_T, {**DECODE, **chunks, "ws_bytes": nb}) == -2
