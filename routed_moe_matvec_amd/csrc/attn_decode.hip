@@ -230,11 +230,11 @@ __device__ __forceinline__ float across8(float x) {
 // of an operand hold each row twice, with two parts of its queries or weights:
 // two products do the work of three.  A score is the sum over a row's two
 // columns (both get it), and so are the sums over values, once, at the end.
-// Matrix and vector instructions of this kernel take their time one after the
-// other (their busy cycles add up to 85 to 97% of all), so fewer products pay:
-// one sequence of 131001 positions, 8 rows a head, 40.1 -> 37.8 us.  With one or
-// two parts of the queries, and only the weights to gain on, it did not: 32
-// sequences of 4 rows in bf16 18.6 -> 18.9 us, of 2 rows in fp16 34.6 -> 34.9.
+// Matrix units are busy 18 to 42% of this kernel's cycles, more than half of that
+// beside no vector work, so fewer products pay: one sequence of 131001 positions, 8
+// rows a head, 40.1 -> 37.8 us.  With one or two parts of the queries, and only the
+// weights to gain on, it did not: 32 sequences of 4 rows in bf16 18.6 -> 18.9 us, of
+// 2 rows in fp16 34.6 -> 34.9.
 template <int TYPE, int DH, int SLOTS>
 __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_decode_kernel(DecodeArgs a) {
     typedef typename ElemOf<TYPE>::type T;

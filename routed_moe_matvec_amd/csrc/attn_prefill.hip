@@ -22,10 +22,10 @@
 // of q . k, not scaled, and is taken off the scores themselves where it is large
 // (RunningMax; 0 to 2% of the time, 3 for 512 queries of 16384 keys).
 //
-// One prompt of 16384 tokens, 32 heads of 128 with 8 key heads, bf16: 2.02 to
-// 2.09 ms, 1053 to 1089 TFLOP/s (a large library product reaches 1219).  The matrix cores are busy
-// 59% of the cycles and the vector units 55%, at a clock that falls as the
-// cycles do (1.9 to 1.7 GHz): the card's power is the limit.
+// One prompt of 16384 tokens, 32 heads of 128 with 8 key heads, bf16: 1.98 to 2.13
+// ms by the card, 1033 to 1111 TFLOP/s (a large library product reaches 1219).  The
+// matrix cores are busy 57% of the cycles, the vector units 47%, both at once 22%, at
+// a clock that falls as the cycles do (1.9 to 1.7 GHz): the card's power is the limit.
 #include <type_traits>
 
 #include "common.h"
@@ -457,15 +457,17 @@ static int launch_prefill_ks(PrefillArgs a, hipStream_t stream) {
 // Where tiles of 128 queries would fill the card at most once (two workgroups a
 // compute unit, one with 256 channels), the waves of a workgroup share 64 or, where
 // those leave compute units without work, 32 queries and split the keys: smaller
-// tiles also spread the triangle of a prompt more evenly.  32 heads of 128, us with
-// 128, 64, 32 queries: 512 of 16384 keys 303, 231; 3 and 20 of 8000 keys 149, -, 87;
-// prompts of 1024 tokens 28.6, 23.9; 3000 94, 106; 16384 2076, 2850; of 768 -, 19, 30.
-// 32 heads of 64: 2048 tokens 36.0, 32.5; 16 heads of 256: 2048 tokens 79, 66; 2500 93,
-// 102.  One round exactly is the border: tiles of one length are even as they are, a
-// prompt's are not.  128 channels, us with 128, 64 queries: 2048 of 16384 keys 500,
-// 561; 2048 tokens 52.5, 52.2, with a window of 600 34.3, 35.7; 8192 of 8 heads 180,
-// 166: tiles of 128.  64 channels: 311, 331; 34.8, 30.9; 22.9, 19.6; 114, 100, and 256:
-// 562, 646; 78, 64; 42, 51; 273, 198: prompts gain more than the others lose.
+// tiles also spread the triangle of a prompt more evenly.  us with 128, 64, 32 queries
+// a workgroup, 32 heads of 128: 128 of 32768 keys 588, 363, 247; 512 of 16384 keys 296,
+// 204, 259; 3 and 20 of 8000 keys 147, 92, 66; prompts of 768 tokens 21.4, 16.5, 27.8; 1024
+// 26.3, 20.6, 39.7; 3000 92, 99, 198; 16384 2117, 2436.  32 heads of 64: 512 tokens 11.7,
+// 8.7, 8.4; 1024 18.3, 13.7, 18.3; 2048 33.4, 30.5, 47.4.  16 heads of 256: 1024 tokens 44.2,
+// 31.5; 2048 78.5, 64.8; 2500 92, 100.  One round exactly is the border: tiles of one
+// length are even as they are, a prompt's are not.  128 channels, us with 128, 64
+// queries: 2048 of 16384 keys 500, 561; 2048 tokens 52.5, 52.2, with a window of 600
+// 34.3, 35.7; 8192 of 8 heads 180, 166: tiles of 128.  64 channels: 311, 331; 34.8, 30.9;
+// 22.9, 19.6; 114, 100, and 256: 562, 646; 78, 64; 42, 51; 273, 198: prompts gain more
+// than the others lose.
 template <int TYPE, int DH>
 static int launch_prefill_dh(const PrefillArgs &a, hipStream_t stream) {
     const long long cus = device_cu_count(), round = DH == 256 ? cus : 2 * cus;
