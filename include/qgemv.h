@@ -126,6 +126,10 @@ extern "C" {
 #define QG_TYPE_F16 1
 #define QG_TYPE_BF16 2
 
+/* which channels of a head the rotation pairs (qk_norm_rope) */
+#define QG_ROPE_HALVES 0     /* i with i + R/2 */
+#define QG_ROPE_NEIGHBOURS 1 /* 2 i with 2 i + 1 */
+
 /* weight formats */
 #define QG_FMT_Q8_0 0
 #define QG_FMT_Q4K 1
@@ -600,6 +604,80 @@ int attn_decode_kv4(int type, const void *q, int ldq, const int32_t *lens, int B
 int attn_prefill(int type, const void *q, int ldq, const void *k, int ldk, const void *v, int ldv, int nq, int nk,
                  const int32_t *cu_q, const int32_t *cu_k, int B, int H, int Hkv, int Dh, float scale, int window,
                  void *y, int32_t *d_status, void *stream);
+
+/*
+ * qk_norm_rope -- what stands between the query/key projections and the cache and
+ * attention calls: the RMS norm of each query and key head and its rotation by the
+ * token's position, in one pass.  q [n, H, Dh] and k [n, Hkv, Dh] are packed new tokens
+ * of B sequences, as kv4_append has them: token cu[b+1]-1 stands at position lens[b]-1.
+ * For a head x of the token at position p (w = wq or wk, fp32 [Dh]; NULL: all ones):
+ *   u_c = x_c / sqrt(mean_c x_c^2 + eps) * w_c
+ *   y_a = u_a cos t - u_b sin t,  y_b = u_b cos t + u_a sin t,  t = p * freq[i], i < R/2,
+ * for the pairs (a, b) = (i, i + R/2) of QG_ROPE_HALVES or (2 i, 2 i + 1) of
+ * QG_ROPE_NEIGHBOURS; y_c = u_c for c >= R.  freq fp32 [R/2] holds radians a position
+ * (may be NULL if R = 0), |p * freq| < 2^31.  q_out [n, H, Dh] and k_out [n, Hkv, Dh] are of
+ * type out_type, which is `type`, or any if that is QG_TYPE_F32; they may be q and k
+ * themselves, with the same row strides, if the types are equal.  Sums and angles: fp32,
+ * but p * freq is taken in 64 bits; the error of an fp32 result is below 2^-18 times the
+ * larger magnitude of its pair, and other types are rounded once.  Squares may be of any size.  Rows of
+ * no sequence, or of one left out by a data error, and parts of rows between the heads and
+ * the stride are not written, nor read with any effect.
+ * Data errors: sequence b is left out (QG_DEV_BAD_LENGTH) if cu[b] < 0, cu[b+1] < cu[b],
+ * cu[b+1] > n, lens[b] < its new tokens or lens[b] >= 2^30; where cu decreases, any other
+ * sequence may be left out too.
+ * Errors: QG_ERR_FORMAT (types, style); QG_ERR_NULL; QG_ERR_SHAPE unless 1 <= n <=
+ * QG_MAX_ATTN_TOKENS, 1 <= B <= QG_MAX_SEQS, 1 <= H, Hkv <= QG_MAX_HEADS, Dh as above,
+ * 0 <= R <= Dh, R % 16 == 0, 2^-100 <= eps <= 2^100, row strides as above, or if
+ * n * ceil((H + Hkv) * Dh / 1024) >= 2^26 - 3 (one launch); QG_ERR_ALIGN; QG_ERR_LAUNCH.
+ */
+int qk_norm_rope(int type, const void *q, int ldq, const void *k, int ldk, int n, const int32_t *cu,
+                 const int32_t *lens, int B, int H, int Hkv, int Dh, const float *wq, const float *wk, float eps,
+                 int R, int style, const float *freq, int out_type, void *q_out, int ldq_out, void *k_out,
+                 int ldk_out, int32_t *d_status, void *stream);
+
+/*
+ * attn_decode_kv4_sinks, attn_prefill_sinks -- attn_decode_kv4 and attn_prefill with a
+ * window and first positions that stay visible: the query at position p sees the keys
+ * j <= p with j > p - window or j < sinks.  window = 0: all j <= p; sinks = 0: the window
+ * alone, bit for bit what the calls without sinks give.  Positions that no query of the call sees are not needed: their
+ * pages, or rows of k and v, may hold anything, and entries of `pages` that name only such
+ * positions are not read, so a serving loop may give back the pages between the sinks and
+ * the window.
+ * ws of the decode call: attn_decode_sinks_workspace_bytes(...) bytes.
+ * Everything else, limits and errors included, as the calls without sinks (QG_ERR_SHAPE
+ * also if sinks < 0).
+ */
+size_t attn_decode_sinks_workspace_bytes(int B, int Tq, int H, int Hkv, int Dh, int max_len, int window, int sinks);
+int attn_decode_kv4_sinks(int type, const void *q, int ldq, const int32_t *lens, int B, int Tq, int H, int Hkv, int Dh,
+                          float scale, int window, int sinks, int max_len, const int32_t *pages, int max_pages,
+                          int page, int num_pages, const void *kv, float *y, void *ws, size_t ws_bytes,
+                          int32_t *d_status, void *stream);
+int attn_prefill_sinks(int type, const void *q, int ldq, const void *k, int ldk, const void *v, int ldv, int nq,
+                       int nk, const int32_t *cu_q, const int32_t *cu_k, int B, int H, int Hkv, int Dh, float scale,
+                       int window, int sinks, void *y, int32_t *d_status, void *stream);
+
+/*
+ * attn_decode_kv4_prefix -- attn_decode_kv4 (without a window) of sequences that have their
+ * first `prefix` positions in common, a system prompt or a question that several answers
+ * continue: the common part is read once, for the queries of all sequences together.
+ * prefix_pages int32 [ceil(prefix / page)] names the pages of positions 0 .. prefix-1;
+ * positions from prefix on of sequence b are in pages[b, position / page] as before, the
+ * block that the prefix ends in among them (a page of the sequence's own, whose
+ * places before prefix % page may hold anything).  Entries of `pages` for blocks before
+ * that one are not read, nor that one where lens[b] <= prefix.  lens[b] and max_len count
+ * the prefix; a sequence may also end inside it (lens[b] = 0 for an unused row of the batch).
+ * prefix = 0 (prefix_pages may be NULL) is attn_decode_kv4.  Results agree with
+ * attn_decode_kv4's over a table whose blocks name the same keys and values to rounding; one
+ * sequence's may depend on the batch by rounding.
+ * ws: attn_decode_prefix_workspace_bytes(...) bytes.
+ * Data errors: as attn_decode_kv4; a bad page of the prefix is left out for all.
+ * Errors: as attn_decode_kv4; QG_ERR_SHAPE unless 0 <= prefix <= max_len.
+ */
+size_t attn_decode_prefix_workspace_bytes(int B, int Tq, int H, int Hkv, int Dh, int max_len, int prefix);
+int attn_decode_kv4_prefix(int type, const void *q, int ldq, const int32_t *lens, int B, int Tq, int H, int Hkv,
+                           int Dh, float scale, int max_len, int prefix, const int32_t *prefix_pages,
+                           const int32_t *pages, int max_pages, int page, int num_pages, const void *kv, float *y,
+                           void *ws, size_t ws_bytes, int32_t *d_status, void *stream);
 
 /* ---- diagnostics ------------------------------------------------------- */
 /* Human-readable text for a QG_* status or QG_DEV_* value (static storage). */

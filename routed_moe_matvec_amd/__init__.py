@@ -22,7 +22,9 @@ __all__ = [
     "qgemv_grouped", "qgemv_q8_0_quality", "FMT_FP8_E4M3_B128", "FMT_FP4_E2M1_MX", "qg_matrix_bytes", "qgemv_mx",
     "moe_routed_qgemv_fmt", "qgemm_q8_0", "qg_stream_read_bursts", "qg_stream_read", "moe_routed_qgemv_noalloc",
     "MOE_SCRATCH_BYTES", "TYPE_F32", "TYPE_F16", "TYPE_BF16", "kv4_page_bytes", "kv4_append", "kv4_gather",
-    "attn_decode_workspace_bytes", "attn_decode_kv4", "attn_prefill",
+    "attn_decode_workspace_bytes", "attn_decode_kv4", "attn_prefill", "ROPE_HALVES", "ROPE_NEIGHBOURS", "qk_norm_rope",
+    "attn_decode_sinks_workspace_bytes", "attn_decode_kv4_sinks", "attn_prefill_sinks",
+    "attn_decode_prefix_workspace_bytes", "attn_decode_kv4_prefix",
 ]
 
 FMT_Q8_0 = 0
@@ -31,6 +33,7 @@ FMT_FP8_E4M3_B128 = 2
 FMT_FP4_E2M1_MX = 3
 DEV_OK, DEV_BAD_EXPERT, DEV_NULL_EXPERT, DEV_BAD_LENGTH, DEV_BAD_PAGE = 0, 1, 2, 3, 4
 TYPE_F32, TYPE_F16, TYPE_BF16 = 0, 1, 2  # QG_TYPE_*
+ROPE_HALVES, ROPE_NEIGHBOURS = 0, 1  # QG_ROPE_*
 MAX_K, MAX_M, MAX_MOE_PAIRS, MAX_EXPERTS = 16384, 32, 8192, 4096
 WS_REGIONS = ["NUNIQ", "UNIQ", "SLOT", "PAIR_OFF", "PAIRS", "G", "V", "H", "HQ", "HD", "HS", "O", "HOT"]
 MOE_MM_PAIRS = 9  # QG_MOE_MM_PAIRS
@@ -103,6 +106,17 @@ _c_decode = _sig("attn_decode_kv4", _i, [_i, _vp, _i, _vp, _i, _i, _i, _i, _i, c
                                          _vp, _vp, _sz, _vp, _vp])
 _c_attn_prefill = _sig("attn_prefill", _i, [_i, _vp, _i, _vp, _i, _vp, _i, _i, _i, _vp, _vp, _i, _i, _i, _i,
                                             ctypes.c_float, _i, _vp, _vp, _vp])
+
+_c_rope = _sig("qk_norm_rope", _i, [_i, _vp, _i, _vp, _i, _i, _vp, _vp, _i, _i, _i, _i, _vp, _vp, ctypes.c_float, _i, _i,
+                                    _vp, _i, _vp, _i, _vp, _i, _vp, _vp])
+_c_decode_sinks_ws = _sig("attn_decode_sinks_workspace_bytes", _sz, [_i] * 8)
+_c_decode_sinks = _sig("attn_decode_kv4_sinks", _i, [_i, _vp, _i, _vp, _i, _i, _i, _i, _i, ctypes.c_float, _i, _i, _i,
+                                                     *_cache_sig, _vp, _vp, _sz, _vp, _vp])
+_c_prefill_sinks = _sig("attn_prefill_sinks", _i, [_i, _vp, _i, _vp, _i, _vp, _i, _i, _i, _vp, _vp, _i, _i, _i, _i,
+                                                   ctypes.c_float, _i, _i, _vp, _vp, _vp])
+_c_decode_prefix_ws = _sig("attn_decode_prefix_workspace_bytes", _sz, [_i] * 7)
+_c_decode_prefix = _sig("attn_decode_kv4_prefix", _i, [_i, _vp, _i, _vp, _i, _i, _i, _i, _i, ctypes.c_float, _i, _i, _vp,
+                                                       *_cache_sig, _vp, _vp, _sz, _vp, _vp])
 
 
 class QGError(RuntimeError):
@@ -400,3 +414,61 @@ def attn_prefill(type: int, q, ldq: int, k, ldk: int, v, ldv: int, nq: int, nk: 
               _rows_ptr(v, "v", dev, type, nk, w, ldv), ldv, nq, nk, _array_ptr(cu_q, "cu_q", dev, _I32, B + 1),
               _array_ptr(cu_k, "cu_k", dev, _I32, B + 1), B, H, Hkv, Dh, scale, window,
               _rows_ptr(y, "y", dev, type, nq, H * Dh, H * Dh), _array_ptr(d_status, "d_status", dev, _I32, 1)), stream)
+
+
+def qk_norm_rope(type: int, q, ldq: int, k, ldk: int, n: int, cu, lens, B: int, H: int, Hkv: int, Dh: int, wq, wk,
+                 eps: float, R: int, style: int, freq, out_type: int, q_out, ldq_out: int, k_out, ldk_out: int, d_status,
+                 stream=None) -> None:
+    wide, w, dev = H * Dh, Hkv * Dh, _device_of(q)
+    _call_on("qk_norm_rope", _c_rope, q, dev,
+             (type, _rows_ptr(q, "q", dev, type, n, wide, ldq), ldq, _rows_ptr(k, "k", dev, type, n, w, ldk), ldk, n,
+              _array_ptr(cu, "cu", dev, _I32, B + 1), _array_ptr(lens, "lens", dev, _I32, B), B, H, Hkv, Dh,
+              _array_ptr(wq, "wq", dev, _FP32, Dh), _array_ptr(wk, "wk", dev, _FP32, Dh), eps, R, style,
+              _array_ptr(freq, "freq", dev, _FP32, R // 2), out_type,
+              _rows_ptr(q_out, "q_out", dev, out_type, n, wide, ldq_out), ldq_out,
+              _rows_ptr(k_out, "k_out", dev, out_type, n, w, ldk_out), ldk_out,
+              _array_ptr(d_status, "d_status", dev, _I32, 1)), stream)
+
+
+def attn_decode_sinks_workspace_bytes(B: int, Tq: int, H: int, Hkv: int, Dh: int, max_len: int, window: int,
+                                      sinks: int) -> int:
+    return int(_c_decode_sinks_ws(B, Tq, H, Hkv, Dh, max_len, window, sinks))
+
+
+def attn_decode_kv4_sinks(type: int, q, ldq: int, lens, B: int, Tq: int, H: int, Hkv: int, Dh: int, scale: float,
+                          window: int, sinks: int, max_len: int, pages, max_pages: int, page: int, num_pages: int, kv, y,
+                          ws, ws_bytes: int, d_status, stream=None) -> None:
+    dev = _device_of(q)
+    _call_on("attn_decode_kv4_sinks", _c_decode_sinks, q, dev,
+             (type, _rows_ptr(q, "q", dev, type, B * Tq, H * Dh, ldq), ldq, _array_ptr(lens, "lens", dev, _I32, B), B,
+              Tq, H, Hkv, Dh, scale, window, sinks, max_len,
+              *_cache_args(dev, pages, B, max_pages, page, num_pages, Hkv, Dh, kv),
+              _array_ptr(y, "y", dev, _FP32, B * Tq * H * Dh), _array_ptr(ws, "ws", dev, None, ws_bytes), ws_bytes,
+              _array_ptr(d_status, "d_status", dev, _I32, 1)), stream)
+
+
+def attn_prefill_sinks(type: int, q, ldq: int, k, ldk: int, v, ldv: int, nq: int, nk: int, cu_q, cu_k, B: int, H: int,
+                       Hkv: int, Dh: int, scale: float, window: int, sinks: int, y, d_status, stream=None) -> None:
+    w, dev = Hkv * Dh, _device_of(q)
+    _call_on("attn_prefill_sinks", _c_prefill_sinks, q, dev,
+             (type, _rows_ptr(q, "q", dev, type, nq, H * Dh, ldq), ldq, _rows_ptr(k, "k", dev, type, nk, w, ldk), ldk,
+              _rows_ptr(v, "v", dev, type, nk, w, ldv), ldv, nq, nk, _array_ptr(cu_q, "cu_q", dev, _I32, B + 1),
+              _array_ptr(cu_k, "cu_k", dev, _I32, B + 1), B, H, Hkv, Dh, scale, window, sinks,
+              _rows_ptr(y, "y", dev, type, nq, H * Dh, H * Dh), _array_ptr(d_status, "d_status", dev, _I32, 1)), stream)
+
+
+def attn_decode_prefix_workspace_bytes(B: int, Tq: int, H: int, Hkv: int, Dh: int, max_len: int, prefix: int) -> int:
+    return int(_c_decode_prefix_ws(B, Tq, H, Hkv, Dh, max_len, prefix))
+
+
+def attn_decode_kv4_prefix(type: int, q, ldq: int, lens, B: int, Tq: int, H: int, Hkv: int, Dh: int, scale: float,
+                           max_len: int, prefix: int, prefix_pages, pages, max_pages: int, page: int, num_pages: int, kv,
+                           y, ws, ws_bytes: int, d_status, stream=None) -> None:
+    dev = _device_of(q)
+    _call_on("attn_decode_kv4_prefix", _c_decode_prefix, q, dev,
+             (type, _rows_ptr(q, "q", dev, type, B * Tq, H * Dh, ldq), ldq, _array_ptr(lens, "lens", dev, _I32, B), B,
+              Tq, H, Hkv, Dh, scale, max_len, prefix,
+              _array_ptr(prefix_pages, "prefix_pages", dev, _I32, -(-prefix // max(page, 1))),
+              *_cache_args(dev, pages, B, max_pages, page, num_pages, Hkv, Dh, kv),
+              _array_ptr(y, "y", dev, _FP32, B * Tq * H * Dh), _array_ptr(ws, "ws", dev, None, ws_bytes), ws_bytes,
+              _array_ptr(d_status, "d_status", dev, _I32, 1)), stream)

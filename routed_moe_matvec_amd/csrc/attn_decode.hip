@@ -68,6 +68,13 @@ inline DecSplit dec_split(int rows, int Dh) {
     return DecSplit{Dh == 64 ? 6 : Dh == 128 ? 7 : 8, least};
 }
 
+// What the positions of a call are:
+//  PLAIN   those up to a query's own, or the last `window` of them
+//  SINKS   the last `window` of them, and the first `sinks`
+//  TAIL    those from `prefix` on, of sequences that share what lies before
+//  PREFIX  those before `prefix`, for the queries of all sequences together
+enum DecMode { PLAIN, SINKS, TAIL, PREFIX };
+
 struct DecodeArgs {
     Kv4Cache c;
     const void *q;
@@ -75,20 +82,39 @@ struct DecodeArgs {
     float *po;   // [B, H * Tq, chunks, Dh] partial sums
     f32x2 *pml;  // [B, H * Tq, chunks] largest q . k and sum
     int ldq, Tq, H, G, window, max_len, chunks;
+    int sinks;
+    int prefix, prefix_log2, prefix_chunks;  // positions, log2 of a chunk's, and the chunks
+    const int32_t *prefix_pages;
     float scale;  // times log2(e), not negative
     float qsign;  // 1, -1 (a negative scale) or 0 (scale 0)
     DecSplit split;
 };
 
-// The visible positions of sequence b's queries are inside [begin, len), begin
-// a multiple of 16; returns their count (0: nothing, or a length out of range).
-__device__ __forceinline__ int dec_range(const DecodeArgs &a, int b, int *len, int *begin) {
-    const int n = load_uniform(a.c.lens + b);
-    *len = n;
-    *begin = 0;
-    if (n < 0 || n > a.max_len) return -1;
-    if (a.window && n - a.Tq - a.window + 1 > 0) *begin = (n - a.Tq - a.window + 1) & ~15;
-    return n - *begin;
+// Where the visible positions of sequence b's queries are.  A kernel counts the
+// places that it walks from 0: places before `edge` are positions 0.., those
+// behind it are `gap` further on.  Both are multiples of 16 (a tile), and the
+// places are all of [0, n); n is negative for a length out of range.
+struct DecRange {
+    int len, edge, gap, n;
+};
+template <int MODE>
+__device__ __forceinline__ DecRange dec_range(const DecodeArgs &a, int b) {
+    DecRange r{load_uniform(a.c.lens + b), 0, 0, -1};
+    if (r.len < 0 || r.len > a.max_len) return r;
+    if (MODE == TAIL) {
+        r.n = 0;
+        if (r.len <= a.prefix) return r;
+        r.gap = a.prefix & ~15;
+    } else if (a.window && r.len - a.Tq - a.window + 1 > 0) {
+        r.gap = (r.len - a.Tq - a.window + 1) & ~15;
+        if (MODE == SINKS) {
+            r.edge = (min(a.sinks, r.len) + 15) & ~15;
+            if (r.gap <= r.edge) r.edge = r.gap = 0;
+            r.gap -= r.edge;
+        }
+    }
+    r.n = r.len - r.gap;
+    return r;
 }
 
 // 8 elements of q as PARTS bf16 vectors whose sum they are.  The first part of
@@ -235,7 +261,7 @@ __device__ __forceinline__ float across8(float x) {
 // rows a head, 40.1 -> 37.8 us.  With one or two parts of the queries, and only the
 // weights to gain on, it did not: 32 sequences of 4 rows in bf16 18.6 -> 18.9 us, of
 // 2 rows in fp16 34.6 -> 34.9.
-template <int TYPE, int DH, int SLOTS>
+template <int TYPE, int DH, int SLOTS, int MODE>
 __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_decode_kernel(DecodeArgs a) {
     typedef typename ElemOf<TYPE>::type T;
     constexpr int QP = kQParts<TYPE>, KC = DH / 32, MT = DH / 16;  // parts of q, key products, channel tiles
@@ -247,19 +273,26 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
     u32x4 *sq = reinterpret_cast<u32x4 *>(&so[0]);
     static_assert(!QLDS || sizeof(so) >= sizeof(u32x4) * QO * KC * kWave, "queries fit the join's room");
     __shared__ f32x2 sml[kDecWaves][16];
-    __shared__ int spage[kDecChunkMax / 16 + 1];
+    __shared__ int spage[kDecChunkMax / 16 + (MODE == SINKS ? 2 : 1)];
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     // sequence by sequence within a chunk number: the workgroups of chunks that a
     // sequence does not have come last
-    const int hk = blockIdx.x % a.c.Hkv, bi = blockIdx.x / a.c.Hkv, b = bi % a.c.B, ci = bi / a.c.B;
+    const int hk = blockIdx.x % a.c.Hkv, bi = blockIdx.x / a.c.Hkv;
+    const int b = MODE == PREFIX ? 0 : bi % a.c.B, ci = MODE == PREFIX ? bi : bi / a.c.B;
     const int row0 = blockIdx.y * ROWS;
-    const int R = a.G * a.Tq;
+    const int R = a.G * a.Tq * (MODE == PREFIX ? a.c.B : 1);
     const int c = lane & 15, g = lane >> 4;
     const int row = row0 + c % ROWS;
     const uint32_t second = c / ROWS ? ~0u : 0u;  // columns of the second, or no, part
     const bool live = row < R;
-    int t = 0;  // the row's token and head
-    for (int i = 1; i < a.Tq; ++i) t += live && row >= i * a.G;
+    // a row's token and head; all sequences' tokens in PREFIX
+    auto token_of = [&](int r) {
+        if (MODE == PREFIX) return r / a.G;
+        int x = 0;
+        for (int i = 1; i < a.Tq; ++i) x += r >= i * a.G;
+        return x;
+    };
+    const int t = live ? token_of(row) : 0;
     const int h = hk * a.G + (live ? row - t * a.G : 0);
     const size_t out_row = (size_t)(b * a.Tq + t) * a.H + h;
 
@@ -276,30 +309,58 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
         }
     }
 
-    int len, begin;
-    const int n = dec_range(a, b, &len, &begin);
-    if (n < 0 && ci == 0 && threadIdx.x == 0) kv4_report(a.c.status, QG_DEV_BAD_LENGTH);
-    const int nchunks = n > 0 ? a.split.chunks(n) : 0;
-    if (ci > 0 && ci >= nchunks) return;
-    if (nchunks == 0) {
-        if (live && wave == 0)
-            for (int i = g * 4; i < DH; i += 16) *(f32x4 *)(a.y + out_row * DH + i) = f32x4{0.f, 0.f, 0.f, 0.f};
-        return;
+    DecRange r;
+    int lg, nchunks;
+    if constexpr (MODE == PREFIX) {
+        r = DecRange{a.prefix, 0, 0, a.prefix};
+        lg = a.prefix_log2;
+        nchunks = a.prefix_chunks;
+    } else {
+        r = dec_range<MODE>(a, b);
+        if (r.n < 0 && ci == 0 && threadIdx.x == 0) kv4_report(a.c.status, QG_DEV_BAD_LENGTH);
+        nchunks = r.n > 0 ? a.split.chunks(r.n) : 0;
+        if ((ci > 0 || MODE == TAIL) && ci >= nchunks) return;
+        if (nchunks == 0) {
+            if (live && wave == 0)
+                for (int i = g * 4; i < DH; i += 16) *(f32x4 *)(a.y + out_row * DH + i) = f32x4{0.f, 0.f, 0.f, 0.f};
+            return;
+        }
+        lg = a.split.chunk_log2(r.n);
     }
-    const int lg = a.split.chunk_log2(n);
-    const int first = begin + (ci << lg), last = min(len, first + (1 << lg));  // this workgroup's positions
+    const int first = ci << lg, last = min(r.n, first + (1 << lg));  // this workgroup's places
     const int page = 1 << a.c.page_log2;
-    const int pos = len - a.Tq + t;                       // this row's position
-    const int see_hi = live ? pos + 1 : 0, see_lo = a.window ? max(pos - a.window + 1, 0) : 0;
-    const uint32_t seen_here = (uint32_t)max(min(see_hi, last) - see_lo, 0);  // positions from see_lo on
-    const int seen = a.window ? len - a.Tq - a.window + 1 : 0;  // the first position that a row sees
+    // the places that this row sees: [see_lo, see_hi), and with SINKS those before `sinks`
+    int see_hi = 0, see_lo = 0, all_hi = r.n - a.Tq + 1;  // and the end of what all rows see
+    if constexpr (MODE == PREFIX) {
+        if (live) {
+            const int n = a.c.lens[t / a.Tq];
+            if (n >= 0 && n <= a.max_len) see_hi = max(min(n - a.Tq + t % a.Tq + 1, a.prefix), 0);
+        }
+        all_hi = live ? see_hi : a.prefix;
+#pragma unroll
+        for (int x = 1; x < 16; x <<= 1) all_hi = min(all_hi, shfl_xor(all_hi, x));
+        all_hi = __builtin_amdgcn_readfirstlane(all_hi);
+    } else {
+        const int pos = r.len - a.Tq + t;
+        see_hi = live ? pos + 1 - r.gap : 0;
+        see_lo = max(a.window ? pos - a.window + 1 - r.gap : 0, MODE == TAIL ? a.prefix - r.gap : r.edge);
+    }
+    const uint32_t seen_here = (uint32_t)max(min(see_hi, last) - see_lo, 0);  // places from see_lo on
+    // the first place, behind the sinks, that a row sees, and the first that all do
+    const int seen = MODE == TAIL ? a.prefix - r.gap : MODE != PREFIX && a.window ? r.n - a.Tq - a.window + 1 : 0;
+    const int all_lo = MODE == TAIL ? a.prefix - r.gap : MODE != PREFIX && a.window ? r.n - a.window : 0;
+    const int sinks = MODE == SINKS ? min(a.sinks, r.n) : 0, sink_hi = min(sinks, see_hi);
     const size_t region = kv4_region_bytes(page, DH);
     const DecLane<DH> ln(lane);
 
-    // the chunk's page ids, through LDS (read by scalar loads a step ahead they made the kernel 5 to 15% slower)
-    const int pg0 = first >> a.c.page_log2;
-    for (int i = threadIdx.x; i <= ((last - 1) >> a.c.page_log2) - pg0; i += kDecWaves * kWave)
-        spage[i] = kv4_page_of(a.c, b, pg0 + i);
+    // the chunk's page ids, through LDS (read by scalar loads a step ahead they made the kernel 5 to 15% slower):
+    // those of places before the edge, which begin with page pg_sink, then the others, from pg0 on
+    const int pg_sink = first >> a.c.page_log2;
+    const int n_sink = MODE == SINKS && first < r.edge ? ((min(last, r.edge) - 1) >> a.c.page_log2) - pg_sink + 1 : 0;
+    const int pg0 = ((MODE == SINKS ? max(first, r.edge) : first) + r.gap) >> a.c.page_log2;
+    const int n_pages = MODE == SINKS && last <= r.edge ? n_sink : n_sink + ((last - 1 + r.gap) >> a.c.page_log2) - pg0 + 1;
+    for (int i = threadIdx.x; i < n_pages; i += kDecWaves * kWave)
+        spage[i] = kv4_page_of(a.c, b, i < n_sink ? pg_sink + i : pg0 + i - n_sink);
     __syncthreads();
 
     // Where a step's two tiles lie; a tile behind the end or on a bad page
@@ -312,10 +373,12 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             const int j0 = j + 16 * x, at = j0 < last ? j0 : first;
-            const int id = __builtin_amdgcn_readfirstlane(spage[(at >> a.c.page_log2) - pg0]);
+            const bool behind = MODE != SINKS || at >= r.edge;
+            const int at_pos = behind ? at + r.gap : at, pg = at_pos >> a.c.page_log2;
+            const int id = __builtin_amdgcn_readfirstlane(spage[behind ? pg - pg0 + n_sink : pg - pg_sink]);
             next_ok[x] = j0 < last && id >= 0;
             at_region[x] = a.c.kv + ((size_t)max(id, 0) * a.c.Hkv + hk) * region;
-            at_off[x] = at & (page - 1);
+            at_off[x] = at_pos & (page - 1);
         }
     };
     auto load_k = [&] {
@@ -395,15 +458,18 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
 #pragma unroll
             for (int i = 0; i < 8; ++i) s[i / 4][i % 4] += across8(s[i / 4][i % 4]);
         // what a row does not see is -inf
-        const bool whole = j + kDecStep <= min(last, len - a.Tq + 1) && cur_ok[0] && cur_ok[1] &&
-                           (!a.window || j >= len - a.window);
+        const bool whole = j + kDecStep <= min(last, all_hi) && cur_ok[0] && cur_ok[1] &&
+                           (j >= all_lo || (MODE == SINKS && j + kDecStep <= sinks));
         if (!whole) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const uint32_t span = cur_ok[x] ? seen_here : 0u;
+                const int upto = cur_ok[x] ? min(sink_hi, last) : 0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if ((uint32_t)(j + 16 * x + 4 * g + i - see_lo) >= span) s[x][i] = -INFINITY;
+                for (int i = 0; i < 4; ++i) {
+                    const int at = j + 16 * x + 4 * g + i;
+                    if ((uint32_t)(at - see_lo) >= span && (MODE != SINKS || at >= upto)) s[x][i] = -INFINITY;
+                }
             }
         }
         float mt = s[0][0];
@@ -451,12 +517,17 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
             }
         }
         // what no row sees may be anything, also its scales: 0 * NaN
-        if (!(j + kDecStep <= last && j >= seen && cur_ok[0] && cur_ok[1])) {
+        if (!(j + kDecStep <= last && (j >= seen || (MODE == SINKS && j + kDecStep <= sinks)) && cur_ok[0] && cur_ok[1])) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const int at = j + 16 * x + 4 * g, left = cur_ok[x] ? last - at : 0, skip = seen - at;
                 uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
-                if (skip > 0) keep = skip >= 4 ? 0u : keep & ~0u << (8 * skip);
+                if (MODE == SINKS) {  // of what is skipped, the sinks stay
+                    auto below = [](int x) { return x >= 4 ? ~0u : x <= 0 ? 0u : (1u << (8 * x)) - 1u; };
+                    keep &= ~below(skip) | below(sinks - at);
+                } else if (skip > 0) {
+                    keep = skip >= 4 ? 0u : keep & ~0u << (8 * skip);
+                }
 #pragma unroll
                 for (int y = 0; y < DecTile<DH>::VC; ++y) cur[x].vs[y] &= keep;
             }
@@ -520,16 +591,16 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
     const int wk = threadIdx.x & 3, wc = (threadIdx.x >> 2) % ROWS, wg = threadIdx.x >> 6;
     const int wi = (threadIdx.x >> 2) % 16 / ROWS * PART;
     const int wrow = row0 + wc;
-    int wt = 0;
-    for (int i = 1; i < a.Tq; ++i) wt += wrow >= i * a.G;
+    const int wt = token_of(wrow);
     const size_t wout = (size_t)(b * a.Tq + wt) * a.H + hk * a.G + wrow - wt * a.G;
     const f32x2 ml = joined(wc);
     float *dst = a.y + wout * DH;
     float f = ml[1] > 0.f ? 1.f / ml[1] : 0.f;
-    if (nchunks > 1) {
-        dst = a.po + (wout * a.chunks + ci) * DH;
+    if (MODE == TAIL || MODE == PREFIX || nchunks > 1) {
+        const int chunk = MODE == TAIL ? a.prefix_chunks + ci : ci;
+        dst = a.po + (wout * a.chunks + chunk) * DH;
         f = 1.f;
-        if (wrow < R && wg == 0 && wk == 0 && wi == 0) a.pml[wout * a.chunks + ci] = ml;
+        if (wrow < R && wg == 0 && wk == 0 && wi == 0) a.pml[wout * a.chunks + chunk] = ml;
     }
 #pragma unroll
     for (int y = 0; y < DecTile<DH>::VC; ++y) {
@@ -565,18 +636,22 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
 // Joins the chunks of sequences that have several: one workgroup per query
 // row, Dh / 4 lanes a chunk, so that 8 to 16 chunks are read at once (one wave
 // per row with a chunk at a time took 20 us for 64 rows of 64 chunks).
-template <int DH>
+template <int DH, int MODE>
 __global__ __launch_bounds__(256) void attn_decode_join_kernel(DecodeArgs a) {
     constexpr int LN = DH / 4, NG = 256 / LN;
     __shared__ __attribute__((aligned(16))) f32x4 so[256];
     __shared__ float sl[NG];
     const int rows = a.H * a.Tq, b = blockIdx.y, row = blockIdx.x, tid = threadIdx.x, lane = lane_id();
-    int len, begin;
-    const int n = dec_range(a, b, &len, &begin);
-    const int nchunks = n > 0 ? a.split.chunks(n) : 0;
-    if (nchunks < 2) return;
+    const int n = dec_range<MODE>(a, b).n, grp = tid / LN, ch = tid % LN;
+    int nchunks = n > 0 ? a.split.chunks(n) : 0;
+    if (MODE == TAIL) {
+        if (n >= 0) nchunks += a.prefix_chunks;
+        if (n < 0 && grp == 0) *(f32x4 *)(a.y + ((size_t)b * rows + row) * DH + ch * 4) = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (n < 0) return;
+    } else if (nchunks < 2) {
+        return;
+    }
     const size_t at = ((size_t)b * rows + row) * a.chunks;
-    const int grp = tid / LN, ch = tid % LN;
     // the first pieces are requested before the maximum is known
     constexpr int PRE = 4;
     const float *po = a.po + at * DH + ch * 4;
@@ -613,19 +688,40 @@ __global__ __launch_bounds__(256) void attn_decode_join_kernel(DecodeArgs a) {
     *(f32x4 *)(a.y + ((size_t)b * rows + row) * DH + ch * 4) = acc * (l > 0.f ? 1.f / l : 0.f);
 }
 
+template <int TYPE, int DH, int MODE>
+static int launch_decode_mode(const DecodeArgs &a, int chunks, hipStream_t stream) {
+    constexpr int SLOTS = kQParts<TYPE> == 3 ? 2 : 1;
+    const int rows = a.G * a.Tq * (MODE == PREFIX ? a.c.B : 1), by = rows <= 16 / SLOTS ? 16 / SLOTS : 16;
+    const long long x = (long long)a.c.Hkv * (MODE == PREFIX ? 1 : a.c.B) * chunks;
+    if ((rows + by - 1) / by > 65535) return QG_ERR_SHAPE;
+    const dim3 grid((unsigned)x, (rows + by - 1) / by), block(kDecWaves * kWave);
+    if (rows <= 16 / SLOTS)
+        hipLaunchKernelGGL((attn_decode_kernel<TYPE, DH, SLOTS, MODE>), grid, block, 0, stream, a);
+    else
+        hipLaunchKernelGGL((attn_decode_kernel<TYPE, DH, 1, MODE>), grid, block, 0, stream, a);
+    return hipGetLastError() == hipSuccess ? QG_OK : QG_ERR_LAUNCH;
+}
+
+template <int DH, int MODE>
+static int launch_join(const DecodeArgs &a, hipStream_t stream) {
+    hipLaunchKernelGGL((attn_decode_join_kernel<DH, MODE>), dim3(a.H * a.Tq, a.c.B), dim3(256), 0, stream, a);
+    return hipGetLastError() == hipSuccess ? QG_OK : QG_ERR_LAUNCH;
+}
+
 template <int TYPE, int DH>
 static int launch_decode_dh(const DecodeArgs &a, hipStream_t stream) {
-    constexpr int SLOTS = kQParts<TYPE> == 3 ? 2 : 1;
-    const int rows = a.G * a.Tq;
-    const dim3 grid((unsigned)((long long)a.c.Hkv * a.c.B * a.chunks), (rows + 15) / 16), block(kDecWaves * kWave);
-    if (rows <= 16 / SLOTS)
-        hipLaunchKernelGGL((attn_decode_kernel<TYPE, DH, SLOTS>), grid, block, 0, stream, a);
-    else
-        hipLaunchKernelGGL((attn_decode_kernel<TYPE, DH, 1>), grid, block, 0, stream, a);
-    if (hipGetLastError() != hipSuccess) return QG_ERR_LAUNCH;
-    if (a.chunks == 1) return QG_OK;
-    hipLaunchKernelGGL(attn_decode_join_kernel<DH>, dim3(a.H * a.Tq, a.c.B), dim3(256), 0, stream, a);
-    return hipGetLastError() == hipSuccess ? QG_OK : QG_ERR_LAUNCH;
+    if (a.prefix) {
+        DecodeArgs p = a;
+        p.c.pages = a.prefix_pages;
+        int rc = launch_decode_mode<TYPE, DH, PREFIX>(p, a.prefix_chunks, stream);
+        if (rc == QG_OK && a.chunks > a.prefix_chunks)
+            rc = launch_decode_mode<TYPE, DH, TAIL>(a, a.chunks - a.prefix_chunks, stream);
+        return rc == QG_OK ? launch_join<DH, TAIL>(a, stream) : rc;
+    }
+    const int rc = a.sinks ? launch_decode_mode<TYPE, DH, SINKS>(a, a.chunks, stream)
+                           : launch_decode_mode<TYPE, DH, PLAIN>(a, a.chunks, stream);
+    if (rc != QG_OK || a.chunks == 1) return rc;
+    return a.sinks ? launch_join<DH, SINKS>(a, stream) : launch_join<DH, PLAIN>(a, stream);
 }
 
 template <int TYPE>
@@ -638,44 +734,55 @@ static int launch_decode(const DecodeArgs &a, int Dh, hipStream_t stream) {
 }
 
 // The workspace: partial sums, then maxima and sums, of every row and chunk.
-static int decode_chunks(int Tq, int G, int Dh, int max_len, int window) {
+struct DecodeChunks {
+    int prefix_log2, prefix, all;  // log2 of a chunk of the prefix, its chunks, and those of prefix and sequence
+};
+static DecodeChunks decode_chunks(int B, int Tq, int G, int Hkv, int Dh, int max_len, int window, int sinks, int prefix) {
+    DecodeChunks n{0, 0, 0};
+    const DecSplit split = dec_split(G * Tq, Dh);
     long long most = max_len;
-    if (window && (long long)window + Tq - 1 + 15 < most) most = (long long)window + Tq - 1 + 15;
-    return dec_split(G * Tq, Dh).chunks_max((int)most);
+    if (prefix) {
+        n.prefix_log2 = split.chunk_log2(prefix);
+        n.prefix = (prefix + (1 << n.prefix_log2) - 1) >> n.prefix_log2;
+        most = max_len > prefix ? max_len - (prefix & ~15) : 0;
+    } else if (window && (long long)window + Tq - 1 + 15 + (sinks + 15LL) / 16 * 16 < most) {
+        most = (long long)window + Tq - 1 + 15 + (sinks + 15LL) / 16 * 16;
+    }
+    n.all = n.prefix + (most ? split.chunks_max((int)most) : 0);
+    return n;
 }
 static size_t decode_sums_bytes(int B, int Tq, int H, int Dh, int chunks) {
     return (size_t)B * Tq * H * chunks * Dh * sizeof(float);
 }
 
-static bool decode_shape_ok(int B, int Tq, int H, int Hkv, int Dh, int max_len, int window) {
+static bool decode_shape_ok(int B, int Tq, int H, int Hkv, int Dh, int max_len, int window, int sinks, int prefix) {
     return B >= 1 && B <= QG_MAX_SEQS && Tq >= 1 && Tq <= QG_MAX_DECODE_TOKENS && H >= 1 && H <= QG_MAX_HEADS &&
            Hkv >= 1 && H % Hkv == 0 && (Dh == 64 || Dh == 128 || Dh == 256) && max_len >= 1 &&
-           max_len <= 0x3fffffff && window >= 0;
+           max_len <= 0x3fffffff && window >= 0 && sinks >= 0 && prefix >= 0 && prefix <= max_len;
 }
 
-}  // namespace qg
-
-extern "C" size_t attn_decode_workspace_bytes(int B, int Tq, int H, int Hkv, int Dh, int max_len, int window) {
-    if (!qg::decode_shape_ok(B, Tq, H, Hkv, Dh, max_len, window)) return 0;
-    const int chunks = qg::decode_chunks(Tq, H / Hkv, Dh, max_len, window);
-    if (chunks == 1) return 256;
-    return qg::decode_sums_bytes(B, Tq, H, Dh, chunks) + (size_t)B * Tq * H * chunks * 2 * sizeof(float);
+static size_t decode_workspace_bytes(int B, int Tq, int H, int Hkv, int Dh, int max_len, int window, int sinks,
+                                     int prefix) {
+    if (!decode_shape_ok(B, Tq, H, Hkv, Dh, max_len, window, sinks, prefix)) return 0;
+    const int chunks = decode_chunks(B, Tq, H / Hkv, Hkv, Dh, max_len, window, sinks, prefix).all;
+    if (chunks == 1 && !prefix) return 256;
+    return decode_sums_bytes(B, Tq, H, Dh, chunks) + (size_t)B * Tq * H * chunks * 2 * sizeof(float);
 }
 
-extern "C" int attn_decode_kv4(int type, const void *q, int ldq, const int32_t *lens, int B, int Tq, int H, int Hkv,
-                               int Dh, float scale, int window, int max_len, const int32_t *pages, int max_pages,
-                               int page, int num_pages, const void *kv, float *y, void *ws, size_t ws_bytes,
-                               int32_t *d_status, void *stream) {
-    using namespace qg;
+static int decode(int type, const void *q, int ldq, const int32_t *lens, int B, int Tq, int H, int Hkv, int Dh,
+                  float scale, int window, int sinks, int max_len, int prefix, const int32_t *prefix_pages,
+                  const int32_t *pages, int max_pages, int page, int num_pages, const void *kv, float *y, void *ws,
+                  size_t ws_bytes, int32_t *d_status, void *stream) {
     if (type != QG_TYPE_F32 && type != QG_TYPE_F16 && type != QG_TYPE_BF16) return QG_ERR_FORMAT;
     if (!q || !lens || !pages || !kv || !y || !ws || !d_status) return QG_ERR_NULL;
-    if (!decode_shape_ok(B, Tq, H, Hkv, Dh, max_len, window)) return QG_ERR_SHAPE;
+    if (!decode_shape_ok(B, Tq, H, Hkv, Dh, max_len, window, sinks, prefix)) return QG_ERR_SHAPE;
     if (!kv4_cache_shape_ok(B, Hkv, Dh, max_pages, page, num_pages) || max_len > (long long)max_pages * page)
         return QG_ERR_SHAPE;
+    if (prefix && !prefix_pages) return QG_ERR_NULL;
     if (!row_stride_ok(type, ldq, H * Dh) || !__builtin_isfinite(2.f * scale)) return QG_ERR_SHAPE;
     if (((uintptr_t)q | (uintptr_t)kv | (uintptr_t)y | (uintptr_t)ws) & 15) return QG_ERR_ALIGN;
-    if (((uintptr_t)lens | (uintptr_t)pages | (uintptr_t)d_status) & 3) return QG_ERR_ALIGN;
-    if (ws_bytes < attn_decode_workspace_bytes(B, Tq, H, Hkv, Dh, max_len, window)) return QG_ERR_WORKSPACE;
+    if (((uintptr_t)lens | (uintptr_t)pages | (uintptr_t)prefix_pages | (uintptr_t)d_status) & 3) return QG_ERR_ALIGN;
+    if (ws_bytes < decode_workspace_bytes(B, Tq, H, Hkv, Dh, max_len, window, sinks, prefix)) return QG_ERR_WORKSPACE;
     DecodeArgs a{};
     a.c.kv = (uint8_t *)const_cast<void *>(kv);
     a.c.pages = pages;
@@ -692,14 +799,21 @@ extern "C" int attn_decode_kv4(int type, const void *q, int ldq, const int32_t *
     a.Tq = Tq;
     a.H = H;
     a.G = H / Hkv;
-    a.window = window < max_len ? window : 0;  // a window as long as a sequence hides nothing
+    // a window that reaches, with the sinks, over a whole sequence hides nothing
+    a.window = (long long)window + sinks < max_len ? window : 0;
+    a.sinks = a.window ? sinks : 0;
     a.max_len = max_len;
+    a.prefix = prefix;
+    a.prefix_pages = prefix_pages;
     a.scale = scale == 0.f ? 1.f : __builtin_fabsf(scale) * 1.44269504088896340736f;
     a.qsign = scale > 0.f ? 1.f : scale < 0.f ? -1.f : 0.f;
-    a.chunks = decode_chunks(Tq, H / Hkv, Dh, max_len, window);
+    const DecodeChunks n = decode_chunks(B, Tq, a.G, Hkv, Dh, max_len, window, sinks, prefix);
+    a.chunks = n.all;
+    a.prefix_chunks = n.prefix;
+    a.prefix_log2 = n.prefix_log2;
     a.split = dec_split(a.G * Tq, Dh);
     a.po = (float *)ws;
-    a.pml = (f32x2 *)((uint8_t *)ws + (a.chunks == 1 ? 0 : decode_sums_bytes(B, Tq, H, Dh, a.chunks)));
+    a.pml = (f32x2 *)((uint8_t *)ws + (a.chunks == 1 && !prefix ? 0 : decode_sums_bytes(B, Tq, H, Dh, a.chunks)));
     if ((long long)Hkv * B * a.chunks * ((a.G * Tq + 15) / 16) > kMaxGroups || (long long)H * Tq * B > kMaxGroups)
         return QG_ERR_SHAPE;
     clear_stale_error();
@@ -708,4 +822,44 @@ extern "C" int attn_decode_kv4(int type, const void *q, int ldq, const int32_t *
         case QG_TYPE_F16: return launch_decode<QG_TYPE_F16>(a, Dh, (hipStream_t)stream);
         default: return launch_decode<QG_TYPE_BF16>(a, Dh, (hipStream_t)stream);
     }
+}
+
+}  // namespace qg
+
+extern "C" size_t attn_decode_workspace_bytes(int B, int Tq, int H, int Hkv, int Dh, int max_len, int window) {
+    return qg::decode_workspace_bytes(B, Tq, H, Hkv, Dh, max_len, window, 0, 0);
+}
+
+extern "C" int attn_decode_kv4(int type, const void *q, int ldq, const int32_t *lens, int B, int Tq, int H, int Hkv,
+                               int Dh, float scale, int window, int max_len, const int32_t *pages, int max_pages,
+                               int page, int num_pages, const void *kv, float *y, void *ws, size_t ws_bytes,
+                               int32_t *d_status, void *stream) {
+    return qg::decode(type, q, ldq, lens, B, Tq, H, Hkv, Dh, scale, window, 0, max_len, 0, nullptr, pages, max_pages,
+                      page, num_pages, kv, y, ws, ws_bytes, d_status, stream);
+}
+
+extern "C" size_t attn_decode_sinks_workspace_bytes(int B, int Tq, int H, int Hkv, int Dh, int max_len, int window,
+                                                    int sinks) {
+    return qg::decode_workspace_bytes(B, Tq, H, Hkv, Dh, max_len, window, sinks, 0);
+}
+
+extern "C" int attn_decode_kv4_sinks(int type, const void *q, int ldq, const int32_t *lens, int B, int Tq, int H,
+                                     int Hkv, int Dh, float scale, int window, int sinks, int max_len,
+                                     const int32_t *pages, int max_pages, int page, int num_pages, const void *kv,
+                                     float *y, void *ws, size_t ws_bytes, int32_t *d_status, void *stream) {
+    return qg::decode(type, q, ldq, lens, B, Tq, H, Hkv, Dh, scale, window, sinks, max_len, 0, nullptr, pages,
+                      max_pages, page, num_pages, kv, y, ws, ws_bytes, d_status, stream);
+}
+
+extern "C" size_t attn_decode_prefix_workspace_bytes(int B, int Tq, int H, int Hkv, int Dh, int max_len, int prefix) {
+    return qg::decode_workspace_bytes(B, Tq, H, Hkv, Dh, max_len, 0, 0, prefix);
+}
+
+extern "C" int attn_decode_kv4_prefix(int type, const void *q, int ldq, const int32_t *lens, int B, int Tq, int H,
+                                      int Hkv, int Dh, float scale, int max_len, int prefix,
+                                      const int32_t *prefix_pages, const int32_t *pages, int max_pages, int page,
+                                      int num_pages, const void *kv, float *y, void *ws, size_t ws_bytes,
+                                      int32_t *d_status, void *stream) {
+    return qg::decode(type, q, ldq, lens, B, Tq, H, Hkv, Dh, scale, 0, 0, max_len, prefix, prefix_pages, pages,
+                      max_pages, page, num_pages, kv, y, ws, ws_bytes, d_status, stream);
 }

@@ -40,7 +40,7 @@ struct PrefillArgs {
     void *y;
     const int32_t *cu_q, *cu_k;
     int32_t *status;
-    int ldq, ldk, ldv, nq, nk, B, H, G, window;
+    int ldq, ldk, ldv, nq, nk, B, H, G, window, sinks;
     float scale;  // times log2(e), not negative
     int flip;     // queries change sign (a negative scale) or vanish (scale 0)
     int slots;    // query tiles, over all sequences, with room to spare
@@ -192,7 +192,12 @@ __device__ __forceinline__ PreWork pre_by_slot(const PrefillArgs &a, int slot) {
 
 // 64 channels with the keys split in two: 128 registers, or a compute unit holds
 // three workgroups in place of four.
-template <int TYPE, int DH, int KS>
+//
+// SINKS: every query sees the first `sinks` keys too.  The keys that a workgroup
+// walks are then counted in places: those before `edge`, a multiple of a tile, are
+// the sinks (the last tile filled up with the last of them, masked), what follows is
+// `gap` further on (or less: the sinks' last tile may reach into it).
+template <int TYPE, int DH, int KS, bool SINKS>
 __global__ __launch_bounds__(kPreWaves *kWave, DH == 256 || KS == 4 ? 1 : DH == 64 && KS == 2 ? 4 : 2) void attn_prefill_kernel(PrefillArgs a) {
     typedef typename ElemOf<TYPE>::type T;
     typedef PreElem<TYPE> E;
@@ -237,6 +242,9 @@ __global__ __launch_bounds__(kPreWaves *kWave, DH == 256 || KS == 4 ? 1 : DH == 
     const int w_hi = min(wi0 + 32, lq) + shift;
     const int qi = min(wi0 + c, lq - 1);
     const int see_hi = qi + shift + 1, see_lo = a.window ? see_hi - a.window : 0;
+    const bool apart = SINKS && wg_lo > a.sinks;
+    const int edge = apart ? (a.sinks + N - 1) / N * N : 0, gap = apart ? wg_lo - edge : 0;
+    const int end = wg_hi - gap;  // the last place, or key
 
     u32x4 qf[KC];
     {
@@ -255,11 +263,15 @@ __global__ __launch_bounds__(kPreWaves *kWave, DH == 256 || KS == 4 ? 1 : DH == 
 
     // A tile's copy: each wave takes every fourth KiB; rows behind the last key repeat it.
     constexpr int RPK = 1024 / (DH * 2), KIB = L::BYTES / 1024;  // rows of a KiB
+    auto key_at = [&](int j0, int r) {
+        if (SINKS && j0 < edge) return min(j0 + r, a.sinks - 1);
+        return min(j0 + gap + r, lk - 1);
+    };
     auto copy_k = [&](int j0, char *sk) {
 #pragma unroll
         for (int i = 0; i < KIB / kPreWaves; ++i) {
             const int kib = i * kPreWaves + wave, r = kib * RPK + lane / L::CH, p = lane % L::CH;
-            global_to_lds16((const T *)a.k + (size_t)(k0 + min(j0 + r, lk - 1)) * a.ldk + hk * DH + 8 * L::k_piece(r, p),
+            global_to_lds16((const T *)a.k + (size_t)(k0 + key_at(j0, r)) * a.ldk + hk * DH + 8 * L::k_piece(r, p),
                             sk + kib * 1024);
         }
     };
@@ -267,7 +279,7 @@ __global__ __launch_bounds__(kPreWaves *kWave, DH == 256 || KS == 4 ? 1 : DH == 
 #pragma unroll
         for (int i = 0; i < KIB / kPreWaves; ++i) {
             const int kib = i * kPreWaves + wave, r = kib * RPK + lane / L::CH, p = lane % L::CH;
-            global_to_lds16((const T *)a.v + (size_t)(k0 + min(j0 + r, lk - 1)) * a.ldv + hk * DH + 8 * L::v_piece(r, p),
+            global_to_lds16((const T *)a.v + (size_t)(k0 + key_at(j0, r)) * a.ldv + hk * DH + 8 * L::v_piece(r, p),
                             sv + kib * 1024);
         }
     };
@@ -309,16 +321,23 @@ __global__ __launch_bounds__(kPreWaves *kWave, DH == 256 || KS == 4 ? 1 : DH == 
                         pf[n][kc][j] = E::pack(s[n][8 * kc + 2 * j], s[n][8 * kc + 2 * j + 1]);
             }
         }
-        const int j0 = next + r0;
+        const int j0 = next + r0 + (SINKS && next < edge ? 0 : gap);
         if constexpr (do_s.value) {
             // register 4 x + y of tile n: key 32 n + 8 x + 4 hf + y
-            if (j0 + OWN > wi0 + shift + 1 || (a.window && j0 < w_hi - a.window)) {
+            if (SINKS && next < edge) {
+                if (j0 + OWN > a.sinks)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (j0 + 32 * n + 8 * (j / 4) + 4 * hf + j % 4 >= a.sinks) t[n][j] = -INFINITY;
+            } else if (j0 + OWN > wi0 + shift + 1 || (a.window && j0 < w_hi - a.window)) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         const int key = j0 + 32 * n + 8 * (j / 4) + 4 * hf + j % 4;
-                        if (key >= see_hi || key < see_lo) t[n][j] = -INFINITY;
+                        if (key >= see_hi || (key < see_lo && (!SINKS || key >= a.sinks))) t[n][j] = -INFINITY;
                     }
             }
         }
@@ -362,15 +381,16 @@ __global__ __launch_bounds__(kPreWaves *kWave, DH == 256 || KS == 4 ? 1 : DH == 
         }
     };
     f32x16 sa[NT], sb[NT];
-    const int first = wg_lo;  // no key that the first query does not see, so none that no query sees
-    if (wg_hi > first) {
+    // no key that the first query does not see, so none that no query sees
+    const int first = SINKS ? 0 : wg_lo;
+    if (end > first) {
         // Before a step its keys (of the next tile) and values have arrived for
         // all waves, and all are done with what the copies begun now replace.
         auto begin = [&](int j, char *sk, char *sv) {
             wait_vmem_all();
             __syncthreads();
-            if (j + 2 * N < wg_hi) copy_k(j + 2 * N, sk);
-            if (j + N < wg_hi) copy_v(j + N, sv);
+            if (j + 2 * N < end) copy_k(j + 2 * N, sk);
+            if (j + N < end) copy_v(j + N, sv);
         };
         copy_k(first, sk0);
         begin(first - N, sk1, sv0);
@@ -378,7 +398,7 @@ __global__ __launch_bounds__(kPreWaves *kWave, DH == 256 || KS == 4 ? 1 : DH == 
         using no = std::false_type;
         step(first, sb, sa, sk0, sv0, yes{}, no{});
         int j = first;
-        for (; j + 2 * N < wg_hi; j += 2 * N) {
+        for (; j + 2 * N < end; j += 2 * N) {
             begin(j, sk0, sv1);
             step(j + N, sa, sb, sk1, sv0, yes{}, yes{});
             begin(j + N, sk1, sv0);
@@ -386,7 +406,7 @@ __global__ __launch_bounds__(kPreWaves *kWave, DH == 256 || KS == 4 ? 1 : DH == 
         }
         begin(j, sk0, sv1);
         const char *sv = sv0;
-        if (j + N < wg_hi) {
+        if (j + N < end) {
             step(j + N, sa, sb, sk1, sv0, yes{}, yes{});
 #pragma unroll
             for (int n = 0; n < NT; ++n) sa[n] = sb[n];
@@ -445,12 +465,12 @@ __global__ __launch_bounds__(kPreWaves *kWave, DH == 256 || KS == 4 ? 1 : DH == 
         }
 }
 
-template <int TYPE, int DH, int KS>
+template <int TYPE, int DH, int KS, bool SINKS>
 static int launch_prefill_ks(PrefillArgs a, hipStream_t stream) {
     a.slots = a.nq / PreTile<DH, KS>::ROWS + a.B;
     const long long grid = (long long)a.slots * a.H;
     if (grid > kMaxGroups) return QG_ERR_SHAPE;
-    hipLaunchKernelGGL((attn_prefill_kernel<TYPE, DH, KS>), dim3((unsigned)grid), dim3(kPreWaves * kWave), 0, stream, a);
+    hipLaunchKernelGGL((attn_prefill_kernel<TYPE, DH, KS, SINKS>), dim3((unsigned)grid), dim3(kPreWaves * kWave), 0, stream, a);
     return hipGetLastError() == hipSuccess ? QG_OK : QG_ERR_LAUNCH;
 }
 
@@ -468,22 +488,47 @@ static int launch_prefill_ks(PrefillArgs a, hipStream_t stream) {
 // 34.3, 35.7; 8192 of 8 heads 180, 166: tiles of 128.  64 channels: 311, 331; 34.8, 30.9;
 // 22.9, 19.6; 114, 100, and 256: 562, 646; 78, 64; 42, 51; 273, 198: prompts gain more
 // than the others lose.
-template <int TYPE, int DH>
+template <int TYPE, int DH, bool SINKS>
 static int launch_prefill_dh(const PrefillArgs &a, hipStream_t stream) {
     const long long cus = device_cu_count(), round = DH == 256 ? cus : 2 * cus;
     const long long tiles = (long long)(a.nq / 128 + a.B / 2) * a.H;  // a sequence's last tile counted half
-    if (tiles > round || (DH == 128 && tiles == round)) return launch_prefill_ks<TYPE, DH, 1>(a, stream);
-    if (DH == 256 || (long long)(a.nq / 64 + a.B) * a.H >= cus) return launch_prefill_ks<TYPE, DH, 2>(a, stream);
-    return launch_prefill_ks<TYPE, DH, DH == 256 ? 2 : 4>(a, stream);
+    if (tiles > round || (DH == 128 && tiles == round)) return launch_prefill_ks<TYPE, DH, 1, SINKS>(a, stream);
+    if (DH == 256 || (long long)(a.nq / 64 + a.B) * a.H >= cus) return launch_prefill_ks<TYPE, DH, 2, SINKS>(a, stream);
+    return launch_prefill_ks<TYPE, DH, DH == 256 ? 2 : 4, SINKS>(a, stream);
 }
 
-template <int TYPE>
+template <int TYPE, bool SINKS>
 static int launch_prefill(const PrefillArgs &a, int Dh, hipStream_t stream) {
     switch (Dh) {
-        case 64: return launch_prefill_dh<TYPE, 64>(a, stream);
-        case 128: return launch_prefill_dh<TYPE, 128>(a, stream);
-        default: return launch_prefill_dh<TYPE, 256>(a, stream);
+        case 64: return launch_prefill_dh<TYPE, 64, SINKS>(a, stream);
+        case 128: return launch_prefill_dh<TYPE, 128, SINKS>(a, stream);
+        default: return launch_prefill_dh<TYPE, 256, SINKS>(a, stream);
     }
+}
+
+static int prefill(int type, const void *q, int ldq, const void *k, int ldk, const void *v, int ldv, int nq, int nk,
+                   const int32_t *cu_q, const int32_t *cu_k, int B, int H, int Hkv, int Dh, float scale, int window,
+                   int sinks, void *y, int32_t *d_status, void *stream) {
+    if (type != QG_TYPE_F16 && type != QG_TYPE_BF16) return QG_ERR_FORMAT;
+    if (!q || !k || !v || !cu_q || !cu_k || !y || !d_status) return QG_ERR_NULL;
+    if (B < 1 || B > QG_MAX_SEQS || H < 1 || H > QG_MAX_HEADS || Hkv < 1 || H % Hkv != 0 ||
+        (Dh != 64 && Dh != 128 && Dh != 256) || nq < 1 || nq > QG_MAX_ATTN_TOKENS || nk < 1 ||
+        nk > QG_MAX_ATTN_TOKENS || window < 0 || sinks < 0 || !__builtin_isfinite(2.f * scale))
+        return QG_ERR_SHAPE;
+    if (!row_stride_ok(type, ldq, H * Dh) || !row_stride_ok(type, ldk, Hkv * Dh) || !row_stride_ok(type, ldv, Hkv * Dh))
+        return QG_ERR_SHAPE;
+    if (((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)y) & 15) return QG_ERR_ALIGN;
+    if (((uintptr_t)cu_q | (uintptr_t)cu_k | (uintptr_t)d_status) & 3) return QG_ERR_ALIGN;
+    PrefillArgs a{q, k, v, y, cu_q, cu_k, d_status, ldq, ldk, ldv, nq, nk, B, H, H / Hkv};
+    // a window that reaches, with the sinks, over the longest sequence hides nothing
+    a.window = (long long)window + sinks < nk ? window : 0;
+    a.sinks = a.window ? sinks : 0;
+    a.scale = scale == 0.f ? 1.f : __builtin_fabsf(scale) * 1.44269504088896340736f;
+    a.flip = scale == 0.f ? -1 : scale < 0.f;
+    clear_stale_error();
+    hipStream_t s = (hipStream_t)stream;
+    if (type == QG_TYPE_F16) return a.sinks ? launch_prefill<QG_TYPE_F16, true>(a, Dh, s) : launch_prefill<QG_TYPE_F16, false>(a, Dh, s);
+    return a.sinks ? launch_prefill<QG_TYPE_BF16, true>(a, Dh, s) : launch_prefill<QG_TYPE_BF16, false>(a, Dh, s);
 }
 
 }  // namespace qg
@@ -491,22 +536,14 @@ static int launch_prefill(const PrefillArgs &a, int Dh, hipStream_t stream) {
 extern "C" int attn_prefill(int type, const void *q, int ldq, const void *k, int ldk, const void *v, int ldv, int nq,
                             int nk, const int32_t *cu_q, const int32_t *cu_k, int B, int H, int Hkv, int Dh,
                             float scale, int window, void *y, int32_t *d_status, void *stream) {
-    using namespace qg;
-    if (type != QG_TYPE_F16 && type != QG_TYPE_BF16) return QG_ERR_FORMAT;
-    if (!q || !k || !v || !cu_q || !cu_k || !y || !d_status) return QG_ERR_NULL;
-    if (B < 1 || B > QG_MAX_SEQS || H < 1 || H > QG_MAX_HEADS || Hkv < 1 || H % Hkv != 0 ||
-        (Dh != 64 && Dh != 128 && Dh != 256) || nq < 1 || nq > QG_MAX_ATTN_TOKENS || nk < 1 ||
-        nk > QG_MAX_ATTN_TOKENS || window < 0 || !__builtin_isfinite(2.f * scale))
-        return QG_ERR_SHAPE;
-    if (!row_stride_ok(type, ldq, H * Dh) || !row_stride_ok(type, ldk, Hkv * Dh) || !row_stride_ok(type, ldv, Hkv * Dh))
-        return QG_ERR_SHAPE;
-    if (((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)y) & 15) return QG_ERR_ALIGN;
-    if (((uintptr_t)cu_q | (uintptr_t)cu_k | (uintptr_t)d_status) & 3) return QG_ERR_ALIGN;
-    PrefillArgs a{q, k, v, y, cu_q, cu_k, d_status, ldq, ldk, ldv, nq, nk, B, H, H / Hkv,
-                  window < nk ? window : 0};  // a window as long as a sequence hides nothing
-    a.scale = scale == 0.f ? 1.f : __builtin_fabsf(scale) * 1.44269504088896340736f;
-    a.flip = scale == 0.f ? -1 : scale < 0.f;
-    clear_stale_error();
-    if (type == QG_TYPE_F16) return launch_prefill<QG_TYPE_F16>(a, Dh, (hipStream_t)stream);
-    return launch_prefill<QG_TYPE_BF16>(a, Dh, (hipStream_t)stream);
+    return qg::prefill(type, q, ldq, k, ldk, v, ldv, nq, nk, cu_q, cu_k, B, H, Hkv, Dh, scale, window, 0, y, d_status,
+                       stream);
+}
+
+extern "C" int attn_prefill_sinks(int type, const void *q, int ldq, const void *k, int ldk, const void *v, int ldv,
+                                  int nq, int nk, const int32_t *cu_q, const int32_t *cu_k, int B, int H, int Hkv,
+                                  int Dh, float scale, int window, int sinks, void *y, int32_t *d_status,
+                                  void *stream) {
+    return qg::prefill(type, q, ldq, k, ldk, v, ldv, nq, nk, cu_q, cu_k, B, H, Hkv, Dh, scale, window, sinks, y,
+                       d_status, stream);
 }

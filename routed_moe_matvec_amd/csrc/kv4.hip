@@ -70,23 +70,6 @@ __device__ __forceinline__ float quad_max(float x) {
     return __builtin_fmaxf(x, swap(x, std::integral_constant<int, 0x4e>{}));  // lane ^ 2
 }
 
-__device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
-    *(f32x4 *)p = f32x4{x[0], x[1], x[2], x[3]};
-    *(f32x4 *)(p + 4) = f32x4{x[4], x[5], x[6], x[7]};
-}
-__device__ __forceinline__ void store8(_Float16 *p, const float (&x)[8]) {
-    f16x8 a;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = (_Float16)x[i];
-    *(f16x8 *)p = a;
-}
-__device__ __forceinline__ void store8(bf16_t *p, const float (&x)[8]) {
-    bf16x8 a;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = (bf16_t)x[i];
-    *(bf16x8 *)p = a;
-}
-
 __device__ __forceinline__ bool kv4_lengths_ok(const Kv4Move &a, int c0, int c1, int len) {
     return c0 >= 0 && c1 >= c0 && c1 <= a.n && len >= c1 - c0 && len <= a.c.max_pages << a.c.page_log2;
 }

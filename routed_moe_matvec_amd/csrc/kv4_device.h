@@ -91,6 +91,23 @@ __device__ __forceinline__ float elem(const Raw8<bf16_t> &r, int i) {
     return (float)__builtin_bit_cast(bf16x2, (uint32_t)r.w[0][i / 2])[i % 2];
 }
 
+__device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
+    *(f32x4 *)p = f32x4{x[0], x[1], x[2], x[3]};
+    *(f32x4 *)(p + 4) = f32x4{x[4], x[5], x[6], x[7]};
+}
+__device__ __forceinline__ void store8(_Float16 *p, const float (&x)[8]) {
+    f16x8 a;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = (_Float16)x[i];
+    *(f16x8 *)p = a;
+}
+__device__ __forceinline__ void store8(bf16_t *p, const float (&x)[8]) {
+    bf16x8 a;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = (bf16_t)x[i];
+    *(bf16x8 *)p = a;
+}
+
 // Index of the last b in [0, B) with key(b) <= x (0 if none), searched 64 ways
 // at a time by the whole wave: one memory round trip for up to 64 sequences,
 // two for 4096.  x is wave-uniform, key(0) is not read.

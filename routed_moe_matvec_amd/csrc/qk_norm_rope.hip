@@ -1,0 +1,222 @@
+// RMS norm of queries and keys, head by head, and their rotation by position.
+//
+//   u_c = x_c / sqrt(mean_c x_c^2 + eps) * w_c;  a pair (a, b) of channels turns by t = position * freq_i:
+//   y_a = u_a cos t - u_b sin t,  y_b = u_b cos t + u_a sin t;  channels from R on stay u.
+//
+// One pass: a lane holds 16 channels of a head (Dh / 16 lanes a head), whole pairs
+// among them, so the rotation needs no exchange and the norm's sum four steps between
+// neighbours at most.  The angle is taken in 64 bits, exact but for one rounding of
+// position * freq, and brought to within an eighth of a turn; sine and cosine are
+// sums of their power series there, in fp32.  A wave computes those of its token
+// once, a lane each, and shares them through LDS.
+#include <type_traits>
+
+#include "common.h"
+#include "kv4_device.h"
+
+namespace qg {
+
+struct RopeArgs {
+    const void *x[2];       // queries, keys
+    void *y[2];
+    const float *w[2];
+    const float *freq;
+    const int32_t *cu, *lens;
+    int32_t *status;
+    int ldx[2], ldy[2];
+    int n, B, H, heads, R;  // heads: of queries and keys
+    int waves, per;         // waves of a token, groups of heads of a wave
+    float eps;
+};
+
+constexpr int kRopeWaves = 4;
+constexpr int kRopeMaxLen = 0x3fffffff;
+
+// cos and sin of x, of any size below 2^40.
+__device__ __forceinline__ f32x2 cos_sin(double x) {
+    const double n = __builtin_rint(x * 0.63661977236758134308);  // quarter turns
+    // pi / 2 as the sum of two doubles
+    const double r = __builtin_fma(-n, 6.12323399573676588613e-17, __builtin_fma(-n, 1.57079632679489661923, x));
+    const int quarter = (int)(n - 4.0 * __builtin_floor(n * 0.25));
+    const float f = (float)r, z = f * f;  // |f| <= pi / 4: the first term left out is below 2^-28 of the sum
+    float s = __builtin_fmaf(z, 1.f / 362880, -1.f / 5040);
+    s = __builtin_fmaf(z, s, 1.f / 120);
+    s = __builtin_fmaf(z, s, -1.f / 6);
+    s = __builtin_fmaf(z * f, s, f);
+    float c = __builtin_fmaf(z, -1.f / 3628800, 1.f / 40320);
+    c = __builtin_fmaf(z, c, -1.f / 720);
+    c = __builtin_fmaf(z, c, 1.f / 24);
+    c = __builtin_fmaf(z, c, -0.5f);
+    c = __builtin_fmaf(z, c, 1.f);
+    const float cc = quarter & 1 ? s : c, ss = quarter & 1 ? c : s;
+    return f32x2{quarter == 1 || quarter == 2 ? -cc : cc, quarter & 2 ? -ss : ss};
+}
+
+// Sum over the 4, 8 or 16 lanes of a head, the same in each.
+template <int LANES>
+__device__ __forceinline__ float head_sum(float x) {
+    auto from = [](float v, auto ctrl) {
+        return __builtin_bit_cast(
+            float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), decltype(ctrl)::value, 0xf, 0xf, true));
+    };
+    x += from(x, std::integral_constant<int, 0xb1>{});                        // lane ^ 1
+    x += from(x, std::integral_constant<int, 0x4e>{});                        // lane ^ 2
+    if (LANES > 4) x += from(x, std::integral_constant<int, 0x141>{});  // the other four of eight
+    if (LANES > 8) x += from(x, std::integral_constant<int, 0x140>{});  // the other eight of sixteen
+    return x;
+}
+
+__device__ __forceinline__ bool rope_lengths_ok(const RopeArgs &a, int c0, int c1, int len) {
+    return c0 >= 0 && c1 >= c0 && c1 <= a.n && len >= c1 - c0 && len <= kRopeMaxLen;
+}
+
+template <int TIN, int TOUT, int DH, bool NEIGHBOURS, int PER>
+__global__ __launch_bounds__(kRopeWaves *kWave) void qk_norm_rope_kernel(RopeArgs a) {
+    typedef typename ElemOf<TIN>::type T;
+    typedef typename ElemOf<TOUT>::type U;
+    constexpr int LANES = DH / 16, HEADS = kWave / LANES;  // lanes of a head, heads of a group
+    __shared__ __attribute__((aligned(16))) f32x2 turns[kRopeWaves][DH / 2];
+    const int lane = lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wave = blockIdx.x * kRopeWaves + wv;
+    if (blockIdx.x == 0)  // every length once: one out of order may otherwise go unseen
+        for (int b = threadIdx.x; b < a.B; b += kRopeWaves * kWave)
+            if (!rope_lengths_ok(a, a.cu[b], a.cu[b + 1], a.lens[b])) kv4_report(a.status, QG_DEV_BAD_LENGTH);
+    const int tok = wave / a.waves;
+    if (tok >= a.n) return;
+
+    // the lane's channels: pieces of 8 from at[0] and at[1] on, the pairs of frequencies 8 i..
+    const int i = lane % LANES;
+    const bool turned = 8 * i < a.R / 2;
+    const int at0 = NEIGHBOURS || !turned ? 16 * i : 8 * i, at1 = NEIGHBOURS || !turned ? 16 * i + 8 : a.R / 2 + 8 * i;
+    const int head0 = wave % a.waves * a.per * HEADS + lane / LANES;
+    Raw8<T> raw[PER][2];
+#pragma unroll
+    for (int p = 0; p < PER; ++p) {
+        const int h = head0 + p * HEADS;
+        if (p < a.per && h < a.heads) {
+            const T *x = h < a.H ? (const T *)a.x[0] + (size_t)tok * a.ldx[0] + h * DH
+                                 : (const T *)a.x[1] + (size_t)tok * a.ldx[1] + (h - a.H) * DH;
+            raw[p][0] = load8(x + at0);
+            raw[p][1] = load8(x + at1);
+        }
+    }
+    const int b = wave_find_last(a.B, tok, [&](int s) { return a.cu[s]; });
+    const int c0 = load_uniform(a.cu + b), c1 = load_uniform(a.cu + b + 1), len = load_uniform(a.lens + b);
+    if (!rope_lengths_ok(a, c0, c1, len) || tok < c0 || tok >= c1) return;
+    const double pos = (double)(len - c1 + tok);
+#pragma unroll
+    for (int f = 0; f < (DH / 2 + kWave - 1) / kWave; ++f) {
+        const int at = f * kWave + lane;
+        if (at < a.R / 2) turns[wv][at] = cos_sin(pos * (double)a.freq[at]);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+    f32x2 turn[8];
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        const f32x4 t = turned ? *(const f32x4 *)&turns[wv][8 * i + j] : f32x4{1.f, 0.f, 1.f, 0.f};
+        turn[j] = f32x2{t[0], t[1]};
+        turn[j + 1] = f32x2{t[2], t[3]};
+    }
+#pragma unroll
+    for (int p = 0; p < PER; ++p) {
+        const int h = head0 + p * HEADS;
+        if (p >= a.per || h - lane / LANES >= a.heads) break;
+        const bool key = h >= a.H;
+        float x[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j] = elem(raw[p][j / 8], j % 8);
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) sum = __builtin_fmaf(x[j], x[j], sum);
+        sum = head_sum<LANES>(sum);
+        float eps = a.eps;
+        if (TIN != QG_TYPE_F16 && !(sum <= 0x1p126f)) {  // squares beyond fp32: all of it 2^64 times smaller
+            sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                x[j] *= 0x1p-64f;
+                sum = __builtin_fmaf(x[j], x[j], sum);
+            }
+            sum = head_sum<LANES>(sum);
+            eps *= 0x1p-128f;
+        }
+        const float r = 1.f / __builtin_sqrtf(sum * (1.f / DH) + eps);
+        const float *w = a.w[key];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j] *= r;
+        if (w)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[j] *= w[(j < 8 ? at0 : at1) + j % 8];
+        float y[2][8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float &ya = NEIGHBOURS ? y[j / 4][2 * (j % 4)] : y[0][j], &yb = NEIGHBOURS ? y[j / 4][2 * (j % 4) + 1] : y[1][j];
+            const float xa = NEIGHBOURS ? x[2 * j] : x[j], xb = NEIGHBOURS ? x[2 * j + 1] : x[8 + j];
+            ya = __builtin_fmaf(xa, turn[j][0], -(xb * turn[j][1]));
+            yb = __builtin_fmaf(xb, turn[j][0], xa * turn[j][1]);
+        }
+        if (h < a.heads) {
+            U *o = key ? (U *)a.y[1] + (size_t)tok * a.ldy[1] + (h - a.H) * DH : (U *)a.y[0] + (size_t)tok * a.ldy[0] + h * DH;
+            store8(o + at0, y[0]);
+            store8(o + at1, y[1]);
+        }
+    }
+}
+
+template <int TIN, int TOUT, int DH, bool NEIGHBOURS>
+static int launch_rope(RopeArgs a, hipStream_t stream) {
+    const int heads = kWave / (DH / 16), groups = (a.heads + heads - 1) / heads;
+    a.per = 1;
+    a.waves = groups;
+    const long long grid = ((long long)a.n * a.waves + kRopeWaves - 1) / kRopeWaves;
+    hipLaunchKernelGGL((qk_norm_rope_kernel<TIN, TOUT, DH, NEIGHBOURS, 1>), dim3((unsigned)grid), dim3(kRopeWaves * kWave), 0, stream, a);
+    return hipGetLastError() == hipSuccess ? QG_OK : QG_ERR_LAUNCH;
+}
+
+template <int TIN, int TOUT>
+static int launch_rope_types(const RopeArgs &a, int Dh, bool neighbours, hipStream_t s) {
+    switch (Dh) {
+        case 64: return neighbours ? launch_rope<TIN, TOUT, 64, true>(a, s) : launch_rope<TIN, TOUT, 64, false>(a, s);
+        case 128: return neighbours ? launch_rope<TIN, TOUT, 128, true>(a, s) : launch_rope<TIN, TOUT, 128, false>(a, s);
+        default: return neighbours ? launch_rope<TIN, TOUT, 256, true>(a, s) : launch_rope<TIN, TOUT, 256, false>(a, s);
+    }
+}
+
+}  // namespace qg
+
+extern "C" int qk_norm_rope(int type, const void *q, int ldq, const void *k, int ldk, int n, const int32_t *cu,
+                            const int32_t *lens, int B, int H, int Hkv, int Dh, const float *wq, const float *wk,
+                            float eps, int R, int style, const float *freq, int out_type, void *q_out, int ldq_out,
+                            void *k_out, int ldk_out, int32_t *d_status, void *stream) {
+    using namespace qg;
+    if (type != QG_TYPE_F32 && type != QG_TYPE_F16 && type != QG_TYPE_BF16) return QG_ERR_FORMAT;
+    if (out_type != type && (type != QG_TYPE_F32 || (out_type != QG_TYPE_F16 && out_type != QG_TYPE_BF16)))
+        return QG_ERR_FORMAT;
+    if (style != QG_ROPE_HALVES && style != QG_ROPE_NEIGHBOURS) return QG_ERR_FORMAT;
+    if (!q || !k || !cu || !lens || !q_out || !k_out || !d_status || (R > 0 && !freq)) return QG_ERR_NULL;
+    if (n < 1 || n > QG_MAX_ATTN_TOKENS || B < 1 || B > QG_MAX_SEQS || H < 1 || H > QG_MAX_HEADS || Hkv < 1 ||
+        Hkv > QG_MAX_HEADS || (Dh != 64 && Dh != 128 && Dh != 256) || R < 0 || R > Dh || R % 16 != 0 ||
+        !(eps >= 0x1p-100f && eps <= 0x1p100f))
+        return QG_ERR_SHAPE;
+    if (!row_stride_ok(type, ldq, H * Dh) || !row_stride_ok(type, ldk, Hkv * Dh) ||
+        !row_stride_ok(out_type, ldq_out, H * Dh) || !row_stride_ok(out_type, ldk_out, Hkv * Dh))
+        return QG_ERR_SHAPE;
+    if ((long long)n * ((((long long)H + Hkv) * Dh + 1023) / 1024) > 4 * kMaxGroups) return QG_ERR_SHAPE;
+    if (((uintptr_t)q | (uintptr_t)k | (uintptr_t)q_out | (uintptr_t)k_out | (uintptr_t)wq | (uintptr_t)wk) & 15)
+        return QG_ERR_ALIGN;
+    if (((uintptr_t)cu | (uintptr_t)lens | (uintptr_t)freq | (uintptr_t)d_status) & 3) return QG_ERR_ALIGN;
+    RopeArgs a{{q, k}, {q_out, k_out}, {wq, wk}, freq, cu, lens, d_status, {ldq, ldk}, {ldq_out, ldk_out},
+               n, B, H, H + Hkv, R, 0, 0, eps};
+    const bool neighbours = style == QG_ROPE_NEIGHBOURS;
+    hipStream_t s = (hipStream_t)stream;
+    clear_stale_error();
+    if (type == QG_TYPE_BF16) return launch_rope_types<QG_TYPE_BF16, QG_TYPE_BF16>(a, Dh, neighbours, s);
+    if (type == QG_TYPE_F16) return launch_rope_types<QG_TYPE_F16, QG_TYPE_F16>(a, Dh, neighbours, s);
+    switch (out_type) {
+        case QG_TYPE_F32: return launch_rope_types<QG_TYPE_F32, QG_TYPE_F32>(a, Dh, neighbours, s);
+        case QG_TYPE_F16: return launch_rope_types<QG_TYPE_F32, QG_TYPE_F16>(a, Dh, neighbours, s);
+        default: return launch_rope_types<QG_TYPE_F32, QG_TYPE_BF16>(a, Dh, neighbours, s);
+    }
+}
