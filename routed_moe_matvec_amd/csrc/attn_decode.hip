@@ -20,119 +20,9 @@
 // to 3% of the time).
 #include <type_traits>
 
-#include "common.h"
-#include "kv4_device.h"
+#include "attn_decode_device.h"
 
 namespace qg {
-
-constexpr int kDecWaves = 4;
-constexpr int kDecStep = 32;                      // positions a wave takes at a time
-constexpr int kDecChunkMax = 8192;                // most positions of a workgroup (4096 times 128 / 64)
-constexpr float kDecSlack = 8.f;                  // a weight may reach 2^8 before the sums are rescaled
-
-// Positions per workgroup, as a power of two, of a sequence of which n are
-// visible: about 8 sqrt(n) at 128 channels (as many bytes at 64 and 256), so
-// that short sequences still spread over the card and long ones do not spend
-// their time joining; and 64 a query row, up to 1024, since every row adds
-// Dh sums to what a chunk writes and the join reads (32 sequences with 16 rows
-// of 256 channels: 100 us with 1024, 112 with 512; one such sequence of 8000: 22
-// and 17 us).  Up to 640 positions (of 128 channels) are one chunk, which needs no
-// join (32 query and 8 key heads, one sequence of 640: 8.0 -> 7.6 us, 32 of them 12.6
-// -> 8.8; one of 1024 would go from 8.0 to 10.0).  A function of the sequence and
-// the heads alone: a sequence's result is the same in any batch.
-struct DecSplit {
-    int dh_log2, least;  // log2 of the channels, least log2 of a chunk
-    __host__ __device__ int chunk_log2(int n) const {
-        int lg = n <= 5 << (7 + 7 - dh_log2) ? 10 : 8;
-        while (lg < 12 && n >= grows_at(lg)) ++lg;
-        lg += 7 - dh_log2;
-        return lg < least ? least : lg;
-    }
-    __host__ __device__ int grows_at(int lg) const { return 1 << (2 * lg - 5 + 7 - dh_log2); }
-    __host__ __device__ int chunks(int n) const {
-        const int lg = chunk_log2(n);
-        return (n + (1 << lg) - 1) >> lg;
-    }
-    // Most chunks of any n up to `most`: at `most` or just before a chunk grows.
-    int chunks_max(int most) const {
-        int best = chunks(most);
-        for (int lg = 8; lg < 12; ++lg)
-            if (grows_at(lg) - 1 <= most && chunks(grows_at(lg) - 1) > best) best = chunks(grows_at(lg) - 1);
-        return best < 1 ? 1 : best;
-    }
-};
-
-inline DecSplit dec_split(int rows, int Dh) {
-    int least = 8;
-    while (least < 10 && 1 << least < 64 * rows) ++least;
-    return DecSplit{Dh == 64 ? 6 : Dh == 128 ? 7 : 8, least};
-}
-
-// What the positions of a call are:
-//  PLAIN   those up to a query's own, or the last `window` of them
-//  SINKS   the last `window` of them, and the first `sinks`
-//  TAIL    those from `prefix` on, of sequences that share what lies before
-//  PREFIX  those before `prefix`, for the queries of all sequences together
-enum DecMode { PLAIN, SINKS, TAIL, PREFIX };
-
-struct DecodeArgs {
-    Kv4Cache c;
-    const void *q;
-    float *y;
-    float *po;   // [B, H * Tq, chunks, Dh] partial sums
-    f32x2 *pml;  // [B, H * Tq, chunks] largest q . k and sum
-    int ldq, Tq, H, G, window, max_len, chunks;
-    int sinks;
-    int prefix, prefix_log2, prefix_chunks;  // positions, log2 of a chunk's, and the chunks
-    const int32_t *prefix_pages;
-    float scale;  // times log2(e), not negative
-    float qsign;  // 1, -1 (a negative scale) or 0 (scale 0)
-    DecSplit split;
-};
-
-// Where the visible positions of sequence b's queries are.  A kernel counts the
-// places that it walks from 0: places before `edge` are positions 0.., those
-// behind it are `gap` further on.  Both are multiples of 16 (a tile), and the
-// places are all of [0, n); n is negative for a length out of range.
-struct DecRange {
-    int len, edge, gap, n;
-};
-template <int MODE>
-__device__ __forceinline__ DecRange dec_range(const DecodeArgs &a, int b) {
-    DecRange r{load_uniform(a.c.lens + b), 0, 0, -1};
-    if (r.len < 0 || r.len > a.max_len) return r;
-    if (MODE == TAIL) {
-        r.n = 0;
-        if (r.len <= a.prefix) return r;
-        r.gap = a.prefix & ~15;
-    } else if (a.window && r.len - a.Tq - a.window + 1 > 0) {
-        r.gap = (r.len - a.Tq - a.window + 1) & ~15;
-        if (MODE == SINKS) {
-            r.edge = (min(a.sinks, r.len) + 15) & ~15;
-            if (r.gap <= r.edge) r.edge = r.gap = 0;
-            r.gap -= r.edge;
-        }
-    }
-    r.n = r.len - r.gap;
-    return r;
-}
-
-// 8 elements of q as PARTS bf16 vectors whose sum they are.  The first part of
-// fp32's largest numbers is bf16's largest, not Inf.
-template <int PARTS, class T>
-__device__ __forceinline__ void split8(const Raw8<T> &r, float sign, bf16x8 (&out)[PARTS]) {
-    constexpr float kMost = 0x1.fep127f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float x = elem(r, i) * sign;
-#pragma unroll
-        for (int s = 0; s < PARTS; ++s) {
-            const bf16_t h = (bf16_t)(PARTS == 3 && s == 0 ? __builtin_amdgcn_fmed3f(x, -kMost, kMost) : x);
-            out[s][i] = h;
-            x -= (float)h;
-        }
-    }
-}
 
 // A lane's part of one 16-position tile.
 template <int DH>
@@ -189,17 +79,6 @@ __device__ __forceinline__ void dec_load_v(DecTile<DH> &t, uint8_t *r, int page,
     }
 }
 
-// Scale byte i where the conversion takes its exponent from, bits 23..30 (it
-// reads no others).
-__device__ __forceinline__ float scale_of(uint32_t bytes, int i) {
-    return __builtin_bit_cast(float, i < 3 ? bytes << (23 - 8 * i) : bytes >> 1);
-}
-
-template <int B>
-__device__ __forceinline__ uint32_t fp4_pair(uint32_t w, float scale) {
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, B));
-}
-
 __device__ __forceinline__ f32x4 mfma16(const u32x4 &a, const u32x4 &b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
                                                    0, 0);
@@ -219,12 +98,6 @@ __device__ __forceinline__ float row_sum(float x) {
     return x + shfl_xor(x, 32);
 }
 
-// Keeps the loads before it where they are: they would sink to their use.
-__device__ __forceinline__ void stay() {
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-}
-
 // Values of two tiles as the A operands of channel pair (2 B, 2 B + 1) of a
 // 16-byte piece: eight positions of either channel.
 template <int B>
@@ -242,9 +115,6 @@ __device__ __forceinline__ void dec_values(const u32x4 &v0, const u32x4 &v1, con
         (*hi)[i] = __builtin_amdgcn_perm(w[2 * i + 1], w[2 * i], 0x07060302u);
     }
 }
-
-template <int TYPE>
-constexpr int kQParts = TYPE == QG_TYPE_F32 ? 3 : TYPE == QG_TYPE_F16 ? 2 : 1;
 
 // The value of the lane 8 columns further on, of 16.
 __device__ __forceinline__ float across8(float x) {
@@ -278,16 +148,14 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
     // sequence by sequence within a chunk number: the workgroups of chunks that a
     // sequence does not have come last
     const int hk = blockIdx.x % a.c.Hkv, bi = blockIdx.x / a.c.Hkv;
-    const int b = MODE == PREFIX ? 0 : bi % a.c.B, ci = MODE == PREFIX ? bi : bi / a.c.B;
+    const int b = bi % a.c.B, ci = bi / a.c.B;
     const int row0 = blockIdx.y * ROWS;
-    const int R = a.G * a.Tq * (MODE == PREFIX ? a.c.B : 1);
+    const int R = a.G * a.Tq;
     const int c = lane & 15, g = lane >> 4;
     const int row = row0 + c % ROWS;
     const uint32_t second = c / ROWS ? ~0u : 0u;  // columns of the second, or no, part
     const bool live = row < R;
-    // a row's token and head; all sequences' tokens in PREFIX
     auto token_of = [&](int r) {
-        if (MODE == PREFIX) return r / a.G;
         int x = 0;
         for (int i = 1; i < a.Tq; ++i) x += r >= i * a.G;
         return x;
@@ -309,46 +177,25 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
         }
     }
 
-    DecRange r;
-    int lg, nchunks;
-    if constexpr (MODE == PREFIX) {
-        r = DecRange{a.prefix, 0, 0, a.prefix};
-        lg = a.prefix_log2;
-        nchunks = a.prefix_chunks;
-    } else {
-        r = dec_range<MODE>(a, b);
-        if (r.n < 0 && ci == 0 && threadIdx.x == 0) kv4_report(a.c.status, QG_DEV_BAD_LENGTH);
-        nchunks = r.n > 0 ? a.split.chunks(r.n) : 0;
-        if ((ci > 0 || MODE == TAIL) && ci >= nchunks) return;
-        if (nchunks == 0) {
-            if (live && wave == 0)
-                for (int i = g * 4; i < DH; i += 16) *(f32x4 *)(a.y + out_row * DH + i) = f32x4{0.f, 0.f, 0.f, 0.f};
-            return;
-        }
-        lg = a.split.chunk_log2(r.n);
+    const DecRange r = dec_range<MODE>(a, b);
+    if (r.n < 0 && ci == 0 && threadIdx.x == 0) kv4_report(a.c.status, QG_DEV_BAD_LENGTH);
+    const int nchunks = r.n > 0 ? a.split.chunks(r.n) : 0;
+    if ((ci > 0 || MODE == TAIL) && ci >= nchunks) return;
+    if (nchunks == 0) {
+        if (live && wave == 0)
+            for (int i = g * 4; i < DH; i += 16) *(f32x4 *)(a.y + out_row * DH + i) = f32x4{0.f, 0.f, 0.f, 0.f};
+        return;
     }
+    const int lg = a.split.chunk_log2(r.n);
     const int first = ci << lg, last = min(r.n, first + (1 << lg));  // this workgroup's places
     const int page = 1 << a.c.page_log2;
     // the places that this row sees: [see_lo, see_hi), and with SINKS those before `sinks`
-    int see_hi = 0, see_lo = 0, all_hi = r.n - a.Tq + 1;  // and the end of what all rows see
-    if constexpr (MODE == PREFIX) {
-        if (live) {
-            const int n = a.c.lens[t / a.Tq];
-            if (n >= 0 && n <= a.max_len) see_hi = max(min(n - a.Tq + t % a.Tq + 1, a.prefix), 0);
-        }
-        all_hi = live ? see_hi : a.prefix;
-#pragma unroll
-        for (int x = 1; x < 16; x <<= 1) all_hi = min(all_hi, shfl_xor(all_hi, x));
-        all_hi = __builtin_amdgcn_readfirstlane(all_hi);
-    } else {
-        const int pos = r.len - a.Tq + t;
-        see_hi = live ? pos + 1 - r.gap : 0;
-        see_lo = max(a.window ? pos - a.window + 1 - r.gap : 0, MODE == TAIL ? a.prefix - r.gap : r.edge);
-    }
+    const int pos = r.len - a.Tq + t, own = MODE == TAIL ? a.prefix - r.gap : 0;
+    const int see_hi = live ? pos + 1 - r.gap : 0;
+    const int see_lo = max(a.window ? pos - a.window + 1 - r.gap : 0, MODE == TAIL ? own : r.edge);
     const uint32_t seen_here = (uint32_t)max(min(see_hi, last) - see_lo, 0);  // places from see_lo on
     // the first place, behind the sinks, that a row sees, and the first that all do
-    const int seen = MODE == TAIL ? a.prefix - r.gap : MODE != PREFIX && a.window ? r.n - a.Tq - a.window + 1 : 0;
-    const int all_lo = MODE == TAIL ? a.prefix - r.gap : MODE != PREFIX && a.window ? r.n - a.window : 0;
+    const int seen = a.window ? r.n - a.Tq - a.window + 1 : own, all_lo = a.window ? r.n - a.window : own;
     const int sinks = MODE == SINKS ? min(a.sinks, r.n) : 0, sink_hi = min(sinks, see_hi);
     const size_t region = kv4_region_bytes(page, DH);
     const DecLane<DH> ln(lane);
@@ -458,7 +305,7 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
 #pragma unroll
             for (int i = 0; i < 8; ++i) s[i / 4][i % 4] += across8(s[i / 4][i % 4]);
         // what a row does not see is -inf
-        const bool whole = j + kDecStep <= min(last, all_hi) && cur_ok[0] && cur_ok[1] &&
+        const bool whole = j + kDecStep <= min(last, r.n - a.Tq + 1) && cur_ok[0] && cur_ok[1] &&
                            (j >= all_lo || (MODE == SINKS && j + kDecStep <= sinks));
         if (!whole) {
 #pragma unroll
@@ -596,7 +443,7 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_deco
     const f32x2 ml = joined(wc);
     float *dst = a.y + wout * DH;
     float f = ml[1] > 0.f ? 1.f / ml[1] : 0.f;
-    if (MODE == TAIL || MODE == PREFIX || nchunks > 1) {
+    if (MODE == TAIL || nchunks > 1) {
         const int chunk = MODE == TAIL ? a.prefix_chunks + ci : ci;
         dst = a.po + (wout * a.chunks + chunk) * DH;
         f = 1.f;
@@ -691,10 +538,8 @@ __global__ __launch_bounds__(256) void attn_decode_join_kernel(DecodeArgs a) {
 template <int TYPE, int DH, int MODE>
 static int launch_decode_mode(const DecodeArgs &a, int chunks, hipStream_t stream) {
     constexpr int SLOTS = kQParts<TYPE> == 3 ? 2 : 1;
-    const int rows = a.G * a.Tq * (MODE == PREFIX ? a.c.B : 1), by = rows <= 16 / SLOTS ? 16 / SLOTS : 16;
-    const long long x = (long long)a.c.Hkv * (MODE == PREFIX ? 1 : a.c.B) * chunks;
-    if ((rows + by - 1) / by > 65535) return QG_ERR_SHAPE;
-    const dim3 grid((unsigned)x, (rows + by - 1) / by), block(kDecWaves * kWave);
+    const int rows = a.G * a.Tq;
+    const dim3 grid((unsigned)((long long)a.c.Hkv * a.c.B * chunks), (rows + 15) / 16), block(kDecWaves * kWave);
     if (rows <= 16 / SLOTS)
         hipLaunchKernelGGL((attn_decode_kernel<TYPE, DH, SLOTS, MODE>), grid, block, 0, stream, a);
     else
@@ -713,7 +558,7 @@ static int launch_decode_dh(const DecodeArgs &a, hipStream_t stream) {
     if (a.prefix) {
         DecodeArgs p = a;
         p.c.pages = a.prefix_pages;
-        int rc = launch_decode_mode<TYPE, DH, PREFIX>(p, a.prefix_chunks, stream);
+        int rc = launch_attn_prefix(TYPE, DH, p, stream);
         if (rc == QG_OK && a.chunks > a.prefix_chunks)
             rc = launch_decode_mode<TYPE, DH, TAIL>(a, a.chunks - a.prefix_chunks, stream);
         return rc == QG_OK ? launch_join<DH, TAIL>(a, stream) : rc;
@@ -735,20 +580,20 @@ static int launch_decode(const DecodeArgs &a, int Dh, hipStream_t stream) {
 
 // The workspace: partial sums, then maxima and sums, of every row and chunk.
 struct DecodeChunks {
-    int prefix_log2, prefix, all;  // log2 of a chunk of the prefix, its chunks, and those of prefix and sequence
+    PrefixSplit prefix;
+    int all;  // chunks of the prefix and a sequence
 };
 static DecodeChunks decode_chunks(int B, int Tq, int G, int Hkv, int Dh, int max_len, int window, int sinks, int prefix) {
-    DecodeChunks n{0, 0, 0};
+    DecodeChunks n{{0, 0}, 0};
     const DecSplit split = dec_split(G * Tq, Dh);
     long long most = max_len;
     if (prefix) {
-        n.prefix_log2 = split.chunk_log2(prefix);
-        n.prefix = (prefix + (1 << n.prefix_log2) - 1) >> n.prefix_log2;
+        n.prefix = prefix_split((long long)B * Tq * G, Hkv, Dh, prefix);
         most = max_len > prefix ? max_len - (prefix & ~15) : 0;
     } else if (window && (long long)window + Tq - 1 + 15 + (sinks + 15LL) / 16 * 16 < most) {
         most = (long long)window + Tq - 1 + 15 + (sinks + 15LL) / 16 * 16;
     }
-    n.all = n.prefix + (most ? split.chunks_max((int)most) : 0);
+    n.all = n.prefix.chunks + (most ? split.chunks_max((int)most) : 0);
     return n;
 }
 static size_t decode_sums_bytes(int B, int Tq, int H, int Dh, int chunks) {
@@ -809,8 +654,8 @@ static int decode(int type, const void *q, int ldq, const int32_t *lens, int B, 
     a.qsign = scale > 0.f ? 1.f : scale < 0.f ? -1.f : 0.f;
     const DecodeChunks n = decode_chunks(B, Tq, a.G, Hkv, Dh, max_len, window, sinks, prefix);
     a.chunks = n.all;
-    a.prefix_chunks = n.prefix;
-    a.prefix_log2 = n.prefix_log2;
+    a.prefix_chunks = n.prefix.chunks;
+    a.prefix_each = n.prefix.each;
     a.split = dec_split(a.G * Tq, Dh);
     a.po = (float *)ws;
     a.pml = (f32x2 *)((uint8_t *)ws + (a.chunks == 1 && !prefix ? 0 : decode_sums_bytes(B, Tq, H, Dh, a.chunks)));

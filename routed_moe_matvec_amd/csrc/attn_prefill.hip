@@ -93,12 +93,6 @@ __device__ __forceinline__ u32x2 lds_read_column4(const char *p) {
     return __builtin_bit_cast(u32x2, x);
 }
 
-__device__ __forceinline__ float half_max(float x) {
-    const uint32_t u = __builtin_bit_cast(uint32_t, x);
-    const auto p = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-    return __builtin_fmaxf(__builtin_bit_cast(float, (uint32_t)p[0]), __builtin_bit_cast(float, (uint32_t)p[1]));
-}
-
 __device__ __forceinline__ bool pre_lengths_ok(const PrefillArgs &a, int q0, int q1, int k0, int k1) {
     return q0 >= 0 && q1 >= q0 && q1 <= a.nq && k0 >= 0 && k1 >= k0 && k1 <= a.nk;
 }

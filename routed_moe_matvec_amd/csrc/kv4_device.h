@@ -126,6 +126,13 @@ __device__ __forceinline__ int wave_find_last(int B, int x, F key) {
     return __builtin_amdgcn_readfirstlane(lo);
 }
 
+// Maximum over the two lanes that hold one row (32 apart).
+__device__ __forceinline__ float half_max(float x) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, x);
+    const auto p = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return __builtin_fmaxf(__builtin_bit_cast(float, (uint32_t)p[0]), __builtin_bit_cast(float, (uint32_t)p[1]));
+}
+
 // The running maximum of a softmax, of scores q . k that are not scaled yet.  A
 // score s has the weight 2^((s - raw) * scale - muse).  Up to 2^16 (scaled) raw is 0
 // and muse the scaled maximum less `shift`, so that a weight takes one fused

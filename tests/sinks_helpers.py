@@ -45,8 +45,11 @@ def attend(q, k, v, scale, seen):
     return y, a, big
 
 
-def check_decode(y, q, k, v, lens, Tq, scale, window, sinks, hidden=None):
-    """y [B * Tq, H, Dh] against each sequence's k[b], v[b] (float64 arrays); hidden[b]: bool [len], keys of bad pages."""
+def check_decode(y, q, k, v, lens, Tq, scale, window, sinks, hidden=None, prefix=0):
+    """y [B * Tq, H, Dh] against each sequence's k[b], v[b] (float64 arrays); hidden[b]: bool [len], keys of bad pages.
+    Over a shared prefix a weight is two fp16 parts of 2^11 times itself: what is left of the first, rounded again, is off
+    by 2^-24 of it (inside attn_helpers' 2^-18) or by half of fp16's least step, 2^-25, so the weight by 2^-36.  It
+    is divided by a sum of at least one (the key with the running maximum has weight one): 2^-36 of each |v|."""
     for b, n in enumerate(lens):
         kk, vv = (torch.from_numpy(np.ascontiguousarray(x[b])).cuda() for x in (k, v))
         rows = slice(b * Tq, (b + 1) * Tq)
@@ -55,6 +58,8 @@ def check_decode(y, q, k, v, lens, Tq, scale, window, sinks, hidden=None):
             seen = seen & ~hidden[b][None]
         ref, a, big = attend(q[rows].double(), kk, vv, scale, seen)
         err, lim = (y[rows].double() - ref).abs(), ah.decode_tolerance(a, big, n, q.shape[2])
+        if prefix:
+            lim = lim + 2.0**-36 * vv[:prefix].abs().sum(0).repeat_interleave(q.shape[1] // kk.shape[1], 0)
         assert bool((err <= lim).all()), "sequence %d (%d positions): %.3g of the tolerance" % (b, n, float((err / lim).max()))
 
 

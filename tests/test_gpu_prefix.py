@@ -85,7 +85,7 @@ def test_values(qg, prefix, lens, Tq, G, Hkv, Dh, page, type):
     q = sh.normal(23, (len(lens) * Tq, G * Hkv, Dh), ah.TYPES[type])
     y, st = decode(qg, s, q, type, Tq, G * Hkv, 0.7 * Dh**-0.5)
     assert int(st) == 0
-    sh.check_decode(y, q, s.k, s.v, lens, Tq, 0.7 * Dh**-0.5, 0, 0)
+    sh.check_decode(y, q, s.k, s.v, lens, Tq, 0.7 * Dh**-0.5, 0, 0, prefix=prefix)
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.05, 8.0])
@@ -94,7 +94,7 @@ def test_scales_and_rows_apart(qg, scale):
     q = sh.normal(33, (3, 8, 128), torch.bfloat16)
     wide = ah.rows_with_gap(q, 8)
     y, _ = decode(qg, s, wide, 2, 1, 8, scale, ldq=wide.stride(0))
-    sh.check_decode(y, q, s.k, s.v, s.lens, 1, scale, 0, 0)
+    sh.check_decode(y, q, s.k, s.v, s.lens, 1, scale, 0, 0, prefix=s.prefix)
 
 
 @pytest.mark.parametrize("lo,hi,spread", [(7, 9, 1.0), (60, 66, 2.0**60), (185, 190, 2.0**-62)])
@@ -105,7 +105,45 @@ def test_far_scales(qg, lo, hi, spread, Dh):
     for type in (0, 2):
         q = sh.normal(33, (2, 20, Dh), ah.TYPES[type], spread)
         y, _ = decode(qg, s, q, type, 1, 20, 0.1)
-        sh.check_decode(y, q, s.k, s.v, s.lens, 1, 0.1, 0, 0)
+        sh.check_decode(y, q, s.k, s.v, s.lens, 1, 0.1, 0, 0, prefix=s.prefix)
+
+
+@pytest.mark.parametrize("type", [0, 1, 2])
+@pytest.mark.parametrize("lo,hi", [(100, 137), (100, 138), (7, 44), (199, 236), (30, 200)])
+def test_scales_far_apart(qg, lo, hi, type):
+    """Scales over 36 binades (all that fp16 operands hold) and over more, in one chunk, at the ends of the range too."""
+    progress("prefix scales %d..%d type %d" % (lo, hi - 1, type))
+    s = Shared(260, [280, 261, 100], 1, 128, 16, 91, lo, hi)
+    q = sh.normal(93, (3, 16, 128), ah.TYPES[type], 2.0 ** (min(127 - (hi - 1), 0) if type else 127 - (hi - 1)))
+    y, st = decode(qg, s, q, type, 1, 16, 0.5)
+    assert int(st) == 0 and bool(y.isfinite().all())
+    sh.check_decode(y, q, s.k, s.v, s.lens, 1, 0.5, 0, 0, prefix=s.prefix)
+
+
+def test_queries_far_apart(qg):
+    """Elements of one fp32 row over 60 binades: the small ones count where the keys hide the large ones."""
+    s = Shared(200, [210, 201], 1, 64, 16, 95)
+    q = sh.normal(96, (2, 12, 64), torch.float32)
+    q[:, :4, :32] *= 2.0**60
+    q[:, 4:6, 5] *= 2.0**25
+    q[:, 6, 9] = 0
+    for keys in (s.c.k[0], s.c.k[1], s.c.k[2]):  # channels whose keys are all zero
+        keys[..., :6] = 0
+    for b, n in enumerate([200] + [m - 192 for m in s.lens]):
+        codes = np.zeros((n, 1, 64), np.uint8)
+        scales = np.full((n, 1, 2), 127, np.uint8)
+        g = np.random.default_rng(b)
+        codes[..., 6:] = g.integers(0, 16, (n, 1, 58))
+        own = np.arange(n) if b == 0 else np.arange(8, n)
+        s.c.put(b, 0, codes[own], scales[own], own)
+        kv = ah.values(codes, scales)
+        if b == 0:
+            shared = kv
+        else:
+            s.k[b - 1] = np.concatenate([shared, kv[8:]])
+    q[:, :4, 6:32] = 0  # what is left of the large ones meets zeros only
+    y, _ = decode(qg, s, q, 0, 1, 12, 0.3)
+    sh.check_decode(y, q, s.k, s.v, s.lens, 1, 0.3, 0, 0, prefix=200)
 
 
 @pytest.mark.parametrize("type", [0, 1, 2])
@@ -118,7 +156,7 @@ def test_scores_of_any_size(qg, type):
     q[1, 1] = 0
     y, st = decode(qg, s, q, type, 1, 8, 1.0)
     assert int(st) == 0 and bool(y.isfinite().all())
-    sh.check_decode(y, q, s.k, s.v, s.lens, 1, 1.0, 0, 0)
+    sh.check_decode(y, q, s.k, s.v, s.lens, 1, 1.0, 0, 0, prefix=s.prefix)
 
 
 def test_without_a_prefix_as_the_plain_call(qg):
@@ -145,7 +183,7 @@ def test_same_as_tables_that_share_pages(qg):
     qg.attn_decode_kv4(0, q, 1024, torch.tensor(s.lens, dtype=torch.int32, device="cuda"), 3, 1, 8, 2, 128, 0.1, 0, 1300,
                        torch.from_numpy(table).cuda(), mp, page, num, kv, z, ws, nb, st)
     for out in (y, z):
-        sh.check_decode(out, q, s.k, s.v, s.lens, 1, 0.1, 0, 0)
+        sh.check_decode(out, q, s.k, s.v, s.lens, 1, 0.1, 0, 0, prefix=s.prefix)
 
 
 def test_runs_are_alike_and_max_len_has_no_effect(qg):
@@ -174,7 +212,7 @@ def test_data_errors(qg):
         for b in range(3):
             hidden[b][32:48] = True
         hidden[2][160:176] = True
-        sh.check_decode(y, q, s.k, s.v, s.lens, 1, 0.1, 0, 0, hidden)
+        sh.check_decode(y, q, s.k, s.v, s.lens, 1, 0.1, 0, 0, hidden, s.prefix)
     cache = s.device()
     cache[0][:] = -1
     cache[1][:] = -1
@@ -212,7 +250,8 @@ def test_captured_twice_on_one_workspace_and_on_another_stream(qg):
         for i in range(2):
             call(i)
             assert torch.equal(ys[i], got[i]), (rep, i)
-            sh.check_decode(got[i], qs[i], [k[:n] for k, n in zip(s.k, now)], [v[:n] for v, n in zip(s.v, now)], now, 1, 0.1, 0, 0)
+            sh.check_decode(got[i], qs[i], [k[:n] for k, n in zip(s.k, now)], [v[:n] for v, n in zip(s.v, now)], now, 1, 0.1, 0, 0,
+                            prefix=900)
     stream, other = torch.cuda.Stream(), torch.empty_like(ys[0])
     stream.wait_stream(torch.cuda.current_stream())
     call(0, other, stream=stream)
