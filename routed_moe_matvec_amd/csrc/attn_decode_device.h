@@ -138,7 +138,7 @@ constexpr int kQParts = TYPE == QG_TYPE_F32 ? 3 : TYPE == QG_TYPE_F16 ? 2 : 1;
 
 // attn_prefix.hip: the part of attn_decode_kv4_prefix that the sequences share, `rows`
 // query rows of a key/value head in tiles of prefix_tile_rows, and how it is cut.
-inline int prefix_tile_rows(long long rows, int Dh) { return Dh == 256 || rows <= 32 ? 32 : 64; }
+inline int prefix_tile_rows(long long rows, int Dh) { return rows > 64 ? 128 : rows > 32 || Dh == 256 ? 64 : 32; }
 struct PrefixSplit {
     int each, chunks;  // positions of a chunk, a multiple of 128, and the chunks
 };

@@ -84,15 +84,6 @@ struct PreTile {
     __device__ static int v_piece(int r, int p) { return p ^ (DH == 64 ? (r >> 1 & 1) << 2 : (r & 3) << 2); }
 };
 
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-
-// Four rows of one column each, out of LDS.
-__device__ __forceinline__ u32x2 lds_read_column4(const char *p) {
-    const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (__attribute__((address_space(3))) s16x4 *)const_cast<char *>(p));
-    return __builtin_bit_cast(u32x2, x);
-}
-
 __device__ __forceinline__ bool pre_lengths_ok(const PrefillArgs &a, int q0, int q1, int k0, int k1) {
     return q0 >= 0 && q1 >= q0 && q1 <= a.nq && k0 >= 0 && k1 >= k0 && k1 <= a.nk;
 }

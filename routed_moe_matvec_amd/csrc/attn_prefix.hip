@@ -1,23 +1,27 @@
 // Attention over the positions that all sequences of a batch share.
 //
 // The query rows of all sequences (tokens and heads that read one key/value head) are
-// one matrix against the shared keys.  A workgroup takes 32 NR rows and a chunk of the
-// positions, its four waves 32 positions each at a time, with the running maximum and sum
-// of a softmax:
+// one matrix against the shared keys.  A workgroup takes up to 128 rows and a chunk of the
+// positions, a tile of them at a time, with the running maximum and sum of a softmax:
 //   S^T = K Q^T    (positions x rows),  O^T += V^T P^T   (channels x rows),
-// as v_mfma_f32_32x32x16.  A lane keeps one query row (of each 32) throughout, and the scores
-// that it receives are the weights that it supplies.  Keys and values go from the cache's
-// bytes to operands in registers, once for all rows.
+// as v_mfma_f32_32x32x16.  The cache's bytes are loaded two tiles ahead and become 16-bit
+// operands in one of two LDS stages once for all rows: K is read from there by rows, V by columns
+// (the transposing read), pieces of 16 bytes permuted by the row's number.  A lane keeps
+// one query row throughout, and the scores that it receives are the weights that it supplies.
+//
+// Operands are fp16 where a chunk's scales span no more than fp16 holds exactly, 36 binades, with
+// one power of two taken off all keys and one off all values; a weight, times 2^11, is then two
+// parts (22 bits, or 2^-36 of the row's largest), an fp32 query two (24 bits of what is
+// within 2^26 of the row's largest, else the chunk is not taken so) and an fp16 one itself.  Other
+// chunks, and the keys of bf16 queries, take bf16, which holds every value exactly, and
+// three parts for 24 bits: five and three products in place of four and three, and six.
 #include <type_traits>
 
 #include "attn_decode_device.h"
 
 namespace qg {
 
-constexpr int kPfxStride = kDecWaves * kDecStep;
-
-// Operands: fp16 where a chunk's scales span no more than fp16 holds exactly, with one
-// power of two taken off all keys and off all values; bf16 else.
+// Sixteen-bit operands from codes, and their products.
 template <bool F16>
 struct PfxOps {
     __device__ static f32x16 mfma(u32x4 a, u32x4 b, f32x16 c) {
@@ -34,6 +38,11 @@ struct PfxOps {
             return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, B));
         else
             return fp4_pair<B>(w, scale);
+    }
+    // eight codes of one scale byte
+    __device__ static u32x4 eight(uint32_t w, uint32_t byte) {
+        const float s = __builtin_bit_cast(float, byte << 23);
+        return u32x4{pair<0>(w, s), pair<1>(w, s), pair<2>(w, s), pair<3>(w, s)};
     }
 };
 
@@ -59,24 +68,31 @@ struct ByteRange {
     }
 };
 
-template <int TYPE, int DH, int NR>
-__global__ __launch_bounds__(kDecWaves *kWave, 2) void attn_prefix_kernel(DecodeArgs a) {
+// A workgroup's shape: KS waves share 32 rows, each with its own positions of a tile.
+template <int DH, int KS>
+struct PfxTile {
+    static constexpr int RW = kDecWaves / KS, ROWS = 32 * RW;
+    static constexpr int N = KS == 4 || DH == 64 ? 128 : KS == 1 && DH == 256 ? 32 : 64;  // positions
+    static constexpr int CH = DH / 8, BYTES = N * DH * 2, PER = N * DH / 8192;               // 16-byte pieces that a thread loads of K, and of V
+    __device__ static int k_piece(int r, int p) { return p ^ (r & (CH < 16 ? CH - 1 : 15)); }
+    __device__ static int v_piece(int r, int p) { return p ^ (DH == 64 ? (r >> 1 & 1) << 2 : (r & 3) << 2); }
+};
+
+template <int TYPE, int DH, int KS>
+__global__ __launch_bounds__(kDecWaves *kWave, DH == 256 || KS == 4 ? 1 : 2) void attn_prefix_kernel(DecodeArgs a) {
     typedef typename ElemOf<TYPE>::type T;
-    constexpr int KC = DH / 16, MT = DH / 32, ROWS = 32 * NR;   // key products, channel tiles
-    constexpr int QS = kQParts<TYPE>, QF = QS == 3 ? 2 : 1;      // parts of q in bf16 and in fp16
-    constexpr int JT = MT < 4 ? MT : 4;                          // channel tiles joined at a time
-    constexpr int QBYTES = QS * NR * KC * 1024, JBYTES = 12 * JT * 1024;
-    __shared__ __attribute__((aligned(16))) char room[QBYTES > JBYTES ? QBYTES : JBYTES];
-    u32x4 *sq = reinterpret_cast<u32x4 *>(room);
-    __shared__ f32x2 sml[kDecWaves][NR][32];
-    __shared__ f32x2 sqr[kDecWaves][NR][32];  // largest and least |q| of a row
+    typedef PfxTile<DH, KS> L;
+    constexpr int N = L::N, NT = N / 32 / KS, KC = DH / 16, MT = DH / 32, PER = L::PER;
+    constexpr int QS = kQParts<TYPE>, QF = QS == 3 ? 2 : 1;  // parts of q in bf16 and in fp16
+    __shared__ __attribute__((aligned(16))) char stage[2][2][L::BYTES];
+    __shared__ f32x2 sml[KS][kDecWaves][32];
     __shared__ uint32_t sbytes[2][kDecWaves];
     __shared__ int spage[kDecChunkMax / 16];
-    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int c = lane & 31, hf = lane >> 5;
+    const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int c = lane & 31, hf = lane >> 5, rw = wave % L::RW, ks = KS == 1 ? 0 : wave / L::RW;
 
     // workgroups are dealt to the 8 XCDs in turn: the row tiles of one chunk go to one XCD
-    const int R = a.G * a.Tq * a.c.B, tiles = (R + ROWS - 1) / ROWS, units = a.c.Hkv * a.prefix_chunks;
+    const int R = a.G * a.Tq * a.c.B, tiles = (R + L::ROWS - 1) / L::ROWS, units = a.c.Hkv * a.prefix_chunks;
     int u, rt;
     {
         const int id = blockIdx.x, whole = units / 8 * 8 * tiles;
@@ -90,103 +106,93 @@ __global__ __launch_bounds__(kDecWaves *kWave, 2) void attn_prefix_kernel(Decode
     }
     const int hk = u % a.c.Hkv, ci = u / a.c.Hkv;
     const int first = ci * a.prefix_each, last = min(a.prefix, first + a.prefix_each);
-    const int page = 1 << a.c.page_log2;
+    const int page = 1 << a.c.page_log2, pg0 = first >> a.c.page_log2;
     const size_t region = kv4_region_bytes(page, DH);
 
-    // the wave's pieces of q: of row tile and key product (n, i), every fourth
-    constexpr int QN = NR * KC / kDecWaves;
-    Raw8<T> qraw[QN];
-    int see_hi[NR], all_hi = a.prefix;
-    size_t out_row[NR];
-    bool live[NR];
-    {
-        const T *qp[NR];
-#pragma unroll
-        for (int n = 0; n < NR; ++n) {
-            const int row = rt * ROWS + 32 * n + c;
-            live[n] = row < R;
-            const int t = live[n] ? row / a.G : 0, h = hk * a.G + (live[n] ? row - t * a.G : 0), len = a.c.lens[t / a.Tq];
-            out_row[n] = (size_t)t * a.H + h;
-            qp[n] = (const T *)a.q + (size_t)t * a.ldq + (size_t)h * DH + hf * (DH / 2);
-            see_hi[n] = 0;
-            if (live[n]) {
-                if (len >= 0 && len <= a.max_len) see_hi[n] = max(min(len - a.Tq + t % a.Tq + 1, a.prefix), 0);
-                all_hi = min(all_hi, see_hi[n]);
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < QN; ++k) qraw[k] = load8(qp[k * kDecWaves / KC] + (k * kDecWaves % KC + wave) * 8);
-#pragma unroll
-        for (int x = 1; x < 32; x <<= 1) all_hi = min(all_hi, shfl_xor(all_hi, x));
-        all_hi = __builtin_amdgcn_readfirstlane(all_hi);
+    bool bad = false;
+    for (int i = tid; i <= ((last - 1) >> a.c.page_log2) - pg0; i += kDecWaves * kWave) {
+        const int id = kv4_page_of(a.c, 0, pg0 + i);
+        spage[i] = id;
+        bad |= id < 0;
     }
-    for (int i = threadIdx.x; i <= ((last - 1) >> a.c.page_log2) - (first >> a.c.page_log2); i += kDecWaves * kWave)
-        spage[i] = kv4_page_of(a.c, 0, (first >> a.c.page_log2) + i);
-    __syncthreads();
+    // the lane's row, and what it sees
+    const int row = rt * L::ROWS + 32 * rw + c;
+    const bool live = row < R;
+    const int t = live ? row / a.G : 0, h = hk * a.G + (live ? row - t * a.G : 0), len = a.c.lens[t / a.Tq];
+    const T *qp = (const T *)a.q + (size_t)t * a.ldq + (size_t)h * DH + 8 * hf;
+    Raw8<T> qraw[KC];
+#pragma unroll
+    for (int i = 0; i < KC; ++i) qraw[i] = load8(qp + 16 * i);
+    const int see_hi = live && len >= 0 && len <= a.max_len ? max(min(len - a.Tq + t % a.Tq + 1, last), 0) : 0;
+    int all_hi = live ? see_hi : last;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) all_hi = min(all_hi, shfl_xor(all_hi, x));
+    all_hi = __builtin_amdgcn_readfirstlane(all_hi);
+    const bool any_bad = __syncthreads_or(bad);
 
-    // A step's two tiles of 16 positions; one behind the end or on a bad page reads the
-    // chunk's first place, or page 0, instead and is masked.
-    uint32_t kraw[KC], kscale;
-    u32x4 vraw[2][2];
-    uint32_t vscale[2][2];
-    const uint8_t *at_tile[2];  // the region
-    int at_off[2];
-    bool next_ok[2];
-    auto locate = [&](int j) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int j0 = j + 16 * x, at = j0 < last ? j0 : first;
-            const int id = __builtin_amdgcn_readfirstlane(spage[(at >> a.c.page_log2) - (first >> a.c.page_log2)]);
-            next_ok[x] = j0 < last && id >= 0;
-            at_tile[x] = a.c.kv + ((size_t)max(id, 0) * a.c.Hkv + hk) * region;
-            at_off[x] = at & (page - 1);
-        }
+    // A tile's bytes: keys by 32 channels of a position, values by 8 channels of four.  What lies
+    // behind the end or on a bad page is read at the chunk's first place, or page 0, and has the scale 0.
+    u32x4 kraw[PER], vraw[PER];
+    uint32_t kbyte[PER], vbytes[PER];
+    auto place = [&](int at, int *off) {
+        const int id = spage[(at >> a.c.page_log2) - pg0];
+        *off = at & (page - 1);
+        return a.c.kv + ((size_t)max(id, 0) * a.c.Hkv + hk) * region;
     };
-    auto load_k = [&] {  // of position c, half of the channels
-        const uint8_t *t = c < 16 ? at_tile[0] : at_tile[1];
-        const int off = (c < 16 ? at_off[0] : at_off[1]) + (c & 15);
-        const uint8_t *k = t + (size_t)off * (DH / 2) + hf * (DH / 4);
-        const uint8_t *s = t + (size_t)page * DH + (size_t)off * (DH / 32) + hf * (DH / 64);
+    auto load = [&](int j) {
 #pragma unroll
-        for (int i = 0; i < KC; i += 4) {
-            const u32x4 w = *(const u32x4 *)(k + 4 * i);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) kraw[i + x] = w[x];
-        }
-        if constexpr (DH == 64)
-            kscale = *s;
-        else if constexpr (DH == 128)
-            kscale = *(const uint16_t *)s;
-        else
-            kscale = *(const uint32_t *)s;
-        stay();
-    };
-    auto load_v = [&] {  // channels MT c.. of positions 4 hf.. and 8 + 4 hf.. of each tile
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                const uint8_t *v = at_tile[x] + (size_t)page * (DH / 2) + (size_t)at_off[x] * (DH / 2);
-                const uint8_t *s = at_tile[x] + (size_t)page * (DH + DH / 32) + (size_t)at_off[x] * (DH / 32);
-                vraw[x][y] = *(const u32x4 *)(v + ((2 * y + hf) * (DH / 8) + c * MT / 8) * 16);
-                vscale[x][y] = *(const uint32_t *)(s + ((2 * y + hf) * (DH / 32) + c * MT / 32) * 4);
+        for (int p = 0; p < PER; ++p) {
+            const int x = tid + p * kDecWaves * kWave;
+            int off;
+            {
+                const int at = j + x / (DH / 32), ch = x % (DH / 32);
+                const uint8_t *r = place(at < last ? at : first, &off);
+                kraw[p] = *(const u32x4 *)(r + (size_t)off * (DH / 2) + ch * 16);
+                kbyte[p] = r[(size_t)page * DH + (size_t)off * (DH / 32) + ch];
             }
+            const int at = j + x / (DH / 8) * 4, ch = x % (DH / 8);
+            const uint8_t *r = place(at < last ? at : first, &off);
+            vraw[p] = *(const u32x4 *)(r + (size_t)page * (DH / 2) + ((size_t)(off >> 2) * (DH / 8) + ch) * 16);
+            vbytes[p] = *(const uint32_t *)(r + (size_t)page * (DH + DH / 32) + ((size_t)(off >> 2) * (DH / 32) + (ch >> 2)) * 4);
+        }
         stay();
     };
-    const int j_first = first + wave * kDecStep;
-    locate(j_first);
-    load_k();
-    load_v();
+    const bool whole_pages = !any_bad;
+    int dk = 0, dv = 0;  // powers of two on keys and values
+    auto store = [&](int j, char *sk, char *sv, auto is_fast) {
+        constexpr bool F = is_fast.value, KF = F && TYPE != QG_TYPE_BF16;
+#pragma unroll
+        for (int p = 0; p < PER; ++p) {
+            const int x = tid + p * kDecWaves * kWave;
+            {
+                const int r = x / (DH / 32), ch = x % (DH / 32);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *(u32x4 *)(sk + r * DH * 2 + 16 * L::k_piece(r, 4 * ch + i)) =
+                        PfxOps<KF>::eight(kraw[p][i], KF ? kbyte[p] + dk : kbyte[p]);
+            }
+            const int r = x / (DH / 8) * 4, ch = x % (DH / 8);
+            int there = last - (j + r);  // of the four
+            if (!whole_pages && there > 0 && spage[((j + r) >> a.c.page_log2) - pg0] < 0) there = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t byte = vbytes[p] >> (8 * i) & 255u;
+                *(u32x4 *)(sv + (r + i) * DH * 2 + 16 * L::v_piece(r + i, ch)) =
+                    PfxOps<F>::eight(vraw[p][i], i < there ? (F ? byte + dv : byte) : 0u);
+            }
+        }
+    };
+    load(first);
 
-    // the range of the chunk's scales, and of each row's queries
+    // the range of the chunk's scales
     {
         ByteRange k, v;
-        constexpr int QUADS = DH / 32;  // 16-byte pieces of a tile's scales
+        constexpr int QUADS = DH / 32;  // 16-byte pieces of 16 positions' scales
         const int n = (last - first + 15) / 16 * QUADS;
-        for (int i = threadIdx.x; i < 2 * n; i += kDecWaves * kWave) {
+        for (int i = tid; i < 2 * n; i += kDecWaves * kWave) {
             const bool val = i >= n;
             const int x = val ? i - n : i, j = first + x / QUADS * 16, piece = x % QUADS;
-            const int id = spage[(j >> a.c.page_log2) - (first >> a.c.page_log2)];
+            const int id = spage[(j >> a.c.page_log2) - pg0];
             if (id < 0) continue;
             const uint8_t *p = a.c.kv + ((size_t)id * a.c.Hkv + hk) * region + (size_t)page * (val ? DH + DH / 32 : DH) +
                                (size_t)(j & (page - 1)) * (DH / 32) + piece * 16;
@@ -208,343 +214,287 @@ __global__ __launch_bounds__(kDecWaves *kWave, 2) void attn_prefix_kernel(Decode
         const uint32_t kr = k.of_wave(), vr = v.of_wave();
         if (lane == 0) sbytes[0][wave] = kr, sbytes[1][wave] = vr;
     }
+    float most_q = 0.f, least_q = INFINITY;  // of the row
     if constexpr (TYPE == QG_TYPE_F32) {
 #pragma unroll
-        for (int n = 0; n < NR; ++n) {
-            float most = 0.f, least = INFINITY;
+        for (int i = 0; i < KC; ++i)
 #pragma unroll
-            for (int k = n * QN / NR; k < (n + 1) * QN / NR; ++k)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float x = __builtin_fabsf(elem(qraw[k], e) * a.qsign);
-                    most = __builtin_fmaxf(most, x);
-                    least = __builtin_fminf(least, x > 0.f ? x : INFINITY);
-                }
-            most = half_max(most);
-            least = -half_max(-least);
-            if (hf == 0) sqr[wave][n][c] = f32x2{most, least};
-        }
+            for (int e = 0; e < 8; ++e) {
+                const float x = __builtin_fabsf(elem(qraw[i], e) * a.qsign);
+                most_q = __builtin_fmaxf(most_q, x);
+                least_q = __builtin_fminf(least_q, x > 0.f ? x : INFINITY);
+            }
+        most_q = half_max(most_q);
+        least_q = -half_max(-least_q);
     }
-    __syncthreads();
-    int dk = 0, dv = 0, qexp[NR];  // powers of two on keys and values, off each row's queries
+    int qexp = 0;  // power of two off the row's queries
     bool fast;
     {
+        const int qe = most_q > 0.f ? __builtin_amdgcn_frexp_expf(most_q) - 15 : 0;
+        bool wide = TYPE == QG_TYPE_F32 && least_q * 0x1p26f < most_q;
+        lds_barrier();  // the first tile's loads stay in flight
         int kl = 255, kh = 0, vl = 255, vh = 0;
 #pragma unroll
         for (int w = 0; w < kDecWaves; ++w) {
             kl = min(kl, (int)(sbytes[0][w] & 255u)), kh = max(kh, (int)(sbytes[0][w] >> 8));
             vl = min(vl, (int)(sbytes[1][w] & 255u)), vh = max(vh, (int)(sbytes[1][w] >> 8));
         }
-        // 6 * 2^13 < 65504, and half of 2^-23 is fp16's least: 36 binades
+        // the largest becomes 2^13 (6 * 2^13 < 65504), the least 2^-23 (half of it is fp16's least)
         fast = vh - vl <= 36 && vh > 0;
         dv = 140 - vh;
         if (TYPE != QG_TYPE_BF16) {
             fast = fast && kh - kl <= 36 && kh > 0;
             dk = 140 - kh;
         }
-        const int sexp = __builtin_amdgcn_frexp_expf(a.scale);
-#pragma unroll
-        for (int n = 0; n < NR; ++n) {
-            qexp[n] = 0;
-            if (TYPE == QG_TYPE_F32) {
-                float most = 0.f, least = INFINITY;
-#pragma unroll
-                for (int w = 0; w < kDecWaves; ++w) {
-                    most = __builtin_fmaxf(most, sqr[w][n][c][0]);
-                    least = __builtin_fminf(least, sqr[w][n][c][1]);
-                }
-                // two parts hold 24 bits of what is within 2^26 of the row's largest
-                if (__ballot(least * 0x1p26f < most)) fast = false;
-                if (most > 0.f) qexp[n] = __builtin_amdgcn_frexp_expf(most) - 15;
-            }
-            const int e = sexp + qexp[n] - dk;
-            if (__ballot(e < -100 || e > 100)) fast = false;
-        }
-        fast = __builtin_amdgcn_readfirstlane(fast);
-        if (!fast) {
-            dk = dv = 0;
-#pragma unroll
-            for (int n = 0; n < NR; ++n) qexp[n] = 0;
-        }
-        dk = __builtin_amdgcn_readfirstlane(dk);
-        dv = __builtin_amdgcn_readfirstlane(dv);
+        const int e = __builtin_amdgcn_frexp_expf(a.scale) + qe - dk;
+        wide |= e < -100 || e > 100;
+        fast = !__syncthreads_or(wide || !fast);
+        qexp = fast ? qe : 0;
+        dk = __builtin_amdgcn_readfirstlane(fast ? dk : 0);
+        dv = __builtin_amdgcn_readfirstlane(fast ? dv : 0);
     }
-    float scale[NR];  // of a row's scores as they are computed
-#pragma unroll
-    for (int n = 0; n < NR; ++n) scale[n] = __builtin_ldexpf(a.scale, qexp[n] - dk);
+    const float scale = __builtin_ldexpf(a.scale, qexp - dk);  // of a row's scores as they are computed
 
-    // queries as the B operands: column c of row tile n, channels 8 i + 0..7 of the lane's half
+    u32x4 qf[QF][KC];
 #pragma unroll
-    for (int k = 0; k < QN; ++k) {
-        const int n = k * kDecWaves / KC, i = k * kDecWaves % KC + wave;
-        u32x4 *to = sq + (n * KC + i) * kWave + lane;
-        if (TYPE != QG_TYPE_BF16 && fast) {
-            u32x4 part[2];
+    for (int i = 0; i < KC; ++i) {
+        if constexpr (TYPE == QG_TYPE_BF16) {
+            bf16x8 part[1];
+            split8<1>(qraw[i], a.qsign, part);
+            qf[0][i] = __builtin_bit_cast(u32x4, part[0]);
+        } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float x0 = __builtin_ldexpf(elem(qraw[k], 2 * e) * a.qsign, -qexp[n]);
-                const float x1 = __builtin_ldexpf(elem(qraw[k], 2 * e + 1) * a.qsign, -qexp[n]);
-                const f16x2 h = __builtin_convertvector((f32x2{x0, x1}), f16x2);
-                const f32x2 rest = {x0 - (float)h[0], x1 - (float)h[1]};
-                part[0][e] = __builtin_bit_cast(uint32_t, h);
-                part[1][e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest, f16x2));
+                const float x0 = __builtin_ldexpf(elem(qraw[i], 2 * e) * a.qsign, -qexp);
+                const float x1 = __builtin_ldexpf(elem(qraw[i], 2 * e + 1) * a.qsign, -qexp);
+                const f16x2 hi = __builtin_convertvector((f32x2{x0, x1}), f16x2);
+                qf[0][i][e] = __builtin_bit_cast(uint32_t, hi);
+                if constexpr (QF == 2) {
+                    const f32x2 rest = {x0 - (float)hi[0], x1 - (float)hi[1]};
+                    qf[1][i][e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest, f16x2));
+                }
             }
-#pragma unroll
-            for (int p = 0; p < QF; ++p) to[p * NR * KC * kWave] = part[p];
-        } else {
-            bf16x8 part[QS];
-            split8<QS>(qraw[k], a.qsign, part);
-#pragma unroll
-            for (int p = 0; p < QS; ++p) to[p * NR * KC * kWave] = __builtin_bit_cast(u32x4, part[p]);
         }
     }
-    lds_barrier();  // keys and values stay in flight
 
-    f32x16 o[NR][MT];
+    f32x16 o[MT];
 #pragma unroll
-    for (int n = 0; n < NR; ++n)
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int x = 0; x < 16; ++x) o[n][i][x] = 0.f;
-    RunningMax most[NR];
-    float l[NR];
-#pragma unroll
-    for (int n = 0; n < NR; ++n) l[n] = 0.f;
+        for (int x = 0; x < 16; ++x) o[i][x] = 0.f;
+    RunningMax most;
+    float l = 0.f;
 
-    auto step = [&](int j, auto more, auto is_fast) {
+    constexpr int OWN = 32 * NT;  // positions of a tile that are this wave's, from r0 on
+    const int r0 = ks * OWN;
+    auto step = [&](int j, const char *sk, const char *sv, auto is_fast) {
         constexpr bool F = is_fast.value, KF = F && TYPE != QG_TYPE_BF16;
-        constexpr int QP = KF ? QF : QS, PP = F ? 2 : 3;  // parts of queries and weights
+        constexpr int PP = F ? 2 : 3;  // parts of weights
         constexpr float kShift = F ? 11.f : 0.f, kSlack = F ? 4.f : kDecSlack;
-        typedef PfxOps<KF> KOps;
-        typedef PfxOps<F> VOps;
-        const bool cur_ok[2] = {next_ok[0], next_ok[1]};
-        f32x16 s[NR];
+        f32x16 s[NT];
 #pragma unroll
-        for (int n = 0; n < NR; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int x = 0; x < 16; ++x) s[n][x] = 0.f;
-        int ql = lane;
-        asm volatile("" : "+v"(ql));  // or the reads below move out of the loop, into registers
-        const uint32_t ks = KF ? kscale + (uint32_t)(dk * 0x01010101) : kscale;
 #pragma unroll
         for (int i = 0; i < KC; ++i) {
-            const float sc = scale_of(ks, i / 4);
-            const uint32_t w = kraw[i];
-            const u32x4 kf = {KOps::template pair<0>(w, sc), KOps::template pair<1>(w, sc), KOps::template pair<2>(w, sc),
-                              KOps::template pair<3>(w, sc)};
+            bf16x8 slow[QS];  // rare: read and split again at each tile, no registers kept
+            if constexpr (!F && QS > 1) split8<QS>(load8(qp + 16 * i), a.qsign, slow);
 #pragma unroll
-            for (int p = 0; p < QP; ++p)
+            for (int n = 0; n < NT; ++n) {
+                const int r = r0 + 32 * n + c;
+                const u32x4 kf = *(const u32x4 *)(sk + r * DH * 2 + 16 * L::k_piece(r, 2 * i + hf));
+                if constexpr (!F && QS > 1) {
 #pragma unroll
-                for (int n = 0; n < NR; ++n) s[n] = KOps::mfma(kf, sq[((p * NR + n) * KC + i) * kWave + ql], s[n]);
-        }
-        if constexpr (more.value) {
-            locate(j + kPfxStride);
-            load_k();
-        }
-        // register 4 x + y: position j + 8 x + 4 hf + y
-        const bool whole = j + kDecStep <= min(last, all_hi) && cur_ok[0] && cur_ok[1];
-        if (!whole) {
+                    for (int p = 0; p < QS; ++p) s[n] = PfxOps<false>::mfma(kf, __builtin_bit_cast(u32x4, slow[p]), s[n]);
+                } else {
 #pragma unroll
-            for (int n = 0; n < NR; ++n)
-#pragma unroll
-                for (int x = 0; x < 16; ++x)
-                    if (j + 8 * (x / 4) + 4 * hf + x % 4 >= (cur_ok[x / 8] ? min(see_hi[n], last) : 0)) s[n][x] = -INFINITY;
-        }
-#pragma unroll
-        for (int n = 0; n < NR; ++n) {
-            float mt = s[n][0];
-#pragma unroll
-            for (int x = 1; x < 16; ++x) mt = __builtin_fmaxf(mt, s[n][x]);
-            mt = half_max(mt);
-            if (__ballot((mt - most[n].m) * scale[n] > kSlack) | most[n].far) {
-                const float keep = most[n].raise(mt, scale[n], kShift);
-                if (most[n].far) {
-                    const float raw = most[n].raw(scale[n]);
-#pragma unroll
-                    for (int x = 0; x < 16; ++x) s[n][x] -= raw;
+                    for (int p = 0; p < QF; ++p) s[n] = PfxOps<KF>::mfma(kf, qf[p][i], s[n]);
                 }
-                l[n] *= keep;
-#pragma unroll
-                for (int i = 0; i < MT; ++i) o[n][i] *= keep;
             }
         }
-        const bool all_there = j + kDecStep <= last && cur_ok[0] && cur_ok[1];
+        // register 4 x + y of tile n: position 32 n + 8 x + 4 hf + y
+        const int j0 = j + r0;
+        if (j0 + OWN > all_hi || any_bad) {
 #pragma unroll
-        for (int kc = 0; kc < 2; ++kc) {
-            u32x4 pf[NR][PP];
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int n = 0; n < NR; ++n)
+                for (int x = 0; x < 16; ++x)
+                    if (j0 + 32 * n + 8 * (x / 4) + 4 * hf + x % 4 >= see_hi) s[n][x] = -INFINITY;
+            if (any_bad)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const int at = j0 + 32 * n + 16 * y;
+                        if (at < last && spage[(at >> a.c.page_log2) - pg0] < 0)
+#pragma unroll
+                            for (int x = 0; x < 8; ++x) s[n][8 * y + x] = -INFINITY;
+                    }
+        }
+        float mt = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int x = 0; x < 16; ++x) mt = __builtin_fmaxf(mt, s[n][x]);
+        mt = half_max(mt);
+        if (__ballot((mt - most.m) * scale > kSlack) | most.far) {
+            const float keep = most.raise(mt, scale, kShift);
+            if (most.far) {
+                const float raw = most.raw(scale);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) s[n][x] -= raw;
+            }
+            l *= keep;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) o[i] *= keep;
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int kc = 0; kc < 2; ++kc) {
+                u32x4 pf[PP];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    float x0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][8 * kc + 2 * e], scale[n], -most[n].muse));
-                    float x1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][8 * kc + 2 * e + 1], scale[n], -most[n].muse));
-                    l[n] += x0;
-                    l[n] += x1;
+                    float x0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][8 * kc + 2 * e], scale, -most.muse));
+                    float x1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][8 * kc + 2 * e + 1], scale, -most.muse));
+                    l += x0;
+                    l += x1;
                     if constexpr (F) {
-                        const f16x2 h = __builtin_convertvector((f32x2{x0, x1}), f16x2);
-                        const f32x2 rest = {__builtin_fmaf((float)h[0], -1.f, x0), __builtin_fmaf((float)h[1], -1.f, x1)};
-                        pf[n][0][e] = __builtin_bit_cast(uint32_t, h);
-                        pf[n][1][e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest, f16x2));
+                        const f16x2 hi = __builtin_convertvector((f32x2{x0, x1}), f16x2);
+                        const f32x2 rest = {__builtin_fmaf((float)hi[0], -1.f, x0), __builtin_fmaf((float)hi[1], -1.f, x1)};
+                        pf[0][e] = __builtin_bit_cast(uint32_t, hi);
+                        pf[1][e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest, f16x2));
                     } else {
 #pragma unroll
                         for (int p = 0; p < PP; ++p) {  // eight bits at a time, cut off: no rounding
                             const uint32_t b0 = __builtin_bit_cast(uint32_t, x0), b1 = __builtin_bit_cast(uint32_t, x1);
-                            pf[n][p][e] = __builtin_amdgcn_perm(b1, b0, 0x07060302u);
+                            pf[p][e] = __builtin_amdgcn_perm(b1, b0, 0x07060302u);
                             x0 -= __builtin_bit_cast(float, b0 & 0xffff0000u);
                             x1 -= __builtin_bit_cast(float, b1 & 0xffff0000u);
                         }
                     }
                 }
-            float vs[2][4];
-            u32x4 v[2];
+                const int r = r0 + 32 * n + 16 * kc + 4 * hf + (lane & 15) / 4;  // and r + 8
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                uint32_t w = vscale[kc][y], keep = ~0u;
-                if (!all_there) {  // what no row sees may be anything, also its scales: 0 * NaN
-                    const int left = cur_ok[kc] ? last - (j + 16 * kc + 8 * y + 4 * hf) : 0;
-                    keep = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
-                    if (F) w = (w & keep) | (~keep & (uint32_t)((140 - dv) * 0x01010101));
+                for (int i = 0; i < MT; ++i) {
+                    const int p = 4 * i + 2 * (c >> 4) + (lane & 3) / 2;
+                    const int at = r * DH * 2 + 16 * L::v_piece(r, p) + 8 * (lane & 1);
+                    const u32x2 x = lds_read_column4(sv + at), y = lds_read_column4(sv + (at + 8 * DH * 2));
+#pragma unroll
+                    for (int w = 0; w < PP; ++w) o[i] = PfxOps<F>::mfma(u32x4{x[0], x[1], y[0], y[1]}, pf[w], o[i]);
                 }
-                if (F) w += (uint32_t)(dv * 0x01010101);
-                w &= keep;
-#pragma unroll
-                for (int t = 0; t < 4; ++t) vs[y][t] = scale_of(w, t);
-                v[y] = vraw[kc][y];
-                if (DH == 64) v[y] >>= (c & 3) * 8;
-                if (DH == 128) v[y] >>= (c & 1) * 16;
             }
-            auto values = [&](auto pair) {  // channels 2 B, 2 B + 1 of the lane's
-                constexpr int B = pair.value;
-                uint32_t w[8];
-#pragma unroll
-                for (int x = 0; x < 8; ++x) w[x] = VOps::template pair<B>(v[x / 4][x % 4], vs[x / 4][x % 4]);
-                u32x4 lo, hi;
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    lo[x] = __builtin_amdgcn_perm(w[2 * x + 1], w[2 * x], 0x05040100u);
-                    hi[x] = __builtin_amdgcn_perm(w[2 * x + 1], w[2 * x], 0x07060302u);
-                }
-#pragma unroll
-                for (int p = 0; p < PP; ++p)
-#pragma unroll
-                    for (int n = 0; n < NR; ++n) {
-                        o[n][2 * B] = VOps::mfma(lo, pf[n][p], o[n][2 * B]);
-                        o[n][2 * B + 1] = VOps::mfma(hi, pf[n][p], o[n][2 * B + 1]);
-                    }
-            };
-            values(std::integral_constant<int, 0>{});
-            if constexpr (MT > 2) values(std::integral_constant<int, 1>{});
-            if constexpr (MT > 4) {
-                values(std::integral_constant<int, 2>{});
-                values(std::integral_constant<int, 3>{});
-            }
-        }
-        if constexpr (more.value) load_v();
     };
-    // The last step, which loads nothing, apart: loads behind a condition would
-    // make every wait one for all of them.
     auto walk = [&](auto is_fast) {
-        int j = j_first;
-        for (; j + kPfxStride < last; j += kPfxStride) step(j, std::true_type{}, is_fast);
-        step(j, std::false_type{}, is_fast);
+        store(first, stage[0][0], stage[0][1], is_fast);
+        if (first + N < last) load(first + N);
+        int s = 0;
+        for (int j = first; j < last; j += N) {
+            // this tile's operands are there for all waves, and all are done with the other stage
+            lds_barrier();
+            if (j + N < last) {
+                store(j + N, stage[s ^ 1][0], stage[s ^ 1][1], is_fast);
+                if (j + 2 * N < last) load(j + 2 * N);
+            }
+            step(j, stage[s][0], stage[s][1], is_fast);
+            s ^= 1;
+        }
     };
-    if (j_first < last) {
-        if (fast)
-            walk(std::true_type{});
-        else
-            walk(std::false_type{});
-    }
+    if (fast)
+        walk(std::true_type{});
+    else
+        walk(std::false_type{});
 
-    // join the waves: maxima first, then the sums through LDS, a quarter of a tile's registers each
-    const float shift = fast ? 11.f : 0.f, unshift = fast ? 0x1p-11f : 1.f;
-    float keep[NR];
+    const float exact = most.exact(scale, fast ? 11.f : 0.f), unshift = fast ? 0x1p-11f : 1.f;
+    float top = most.m, keep = exact * unshift;
+    l = (l + shfl_xor(l, 32)) * exact;
+    if constexpr (KS > 1) {  // join the waves that share rows, through the stages
+        if (hf == 0) sml[ks][rw][c] = f32x2{most.m, l};
+        __syncthreads();
+        float sum = 0.f;
 #pragma unroll
-    for (int n = 0; n < NR; ++n) {
-        const float exact = most[n].exact(scale[n], shift);
-        l[n] = (l[n] + shfl_xor(l[n], 32)) * exact;
-        keep[n] = exact;
-        if (hf == 0) sml[wave][n][c] = f32x2{most[n].m, l[n]};
-    }
-    __syncthreads();  // and every wave is done with the queries
-#pragma unroll
-    for (int n = 0; n < NR; ++n) {
-        float top = -INFINITY, sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < kDecWaves; ++w) top = __builtin_fmaxf(top, sml[w][n][c][0]);
+        for (int x = 0; x < KS; ++x) top = __builtin_fmaxf(top, sml[x][rw][c][0]);
         const float use = top == -INFINITY ? 0.f : top;
 #pragma unroll
-        for (int w = 0; w < kDecWaves; ++w)
-            sum += sml[w][n][c][1] * __builtin_amdgcn_exp2f((sml[w][n][c][0] - use) * scale[n]);
-        keep[n] *= __builtin_amdgcn_exp2f((most[n].m - use) * scale[n]);
-        const size_t at = out_row[n] * a.chunks + ci;
-        if (wave == 0 && hf == 0 && live[n]) a.pml[at] = f32x2{__builtin_ldexpf(top, qexp[n] - dk), sum * unshift};
-        f32x4 *part = reinterpret_cast<f32x4 *>(room);  // [wave][quarter - 1 or quarter][tile][lane]
+        for (int x = 0; x < KS; ++x) sum += sml[x][rw][c][1] * __builtin_amdgcn_exp2f((sml[x][rw][c][0] - use) * scale);
+        keep *= __builtin_amdgcn_exp2f((most.m - use) * scale);
+        l = sum;
+        static_assert(sizeof(stage) >= (KS - 1) * L::RW * 32 * DH * 4, "the waves' sums fit the stages");
+        f32x4 *room = reinterpret_cast<f32x4 *>(&stage[0][0][0]);
 #pragma unroll
-        for (int i0 = 0; i0 < MT; i0 += JT) {
-            if (n || i0) __syncthreads();
-            f32x4 mine[JT];
+        for (int i = 0; i < MT; ++i) o[i] *= keep;
+        keep = 1.f;
+        if (ks > 0)
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
+            for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int i = 0; i < JT; ++i) {
-                    f32x4 v;
+                for (int x = 0; x < 4; ++x)
+                    room[(((ks - 1) * L::RW + rw) * MT * 4 + 4 * i + x) * kWave + lane] =
+                        f32x4{o[i][4 * x], o[i][4 * x + 1], o[i][4 * x + 2], o[i][4 * x + 3]};
+        __syncthreads();
+        if (ks > 0) return;
+        for (int y = 1; y < KS; ++y)
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) v[y] = o[n][i0 + i][4 * x + y] * keep[n];
-                    if (x == wave)
-                        mine[i] = v;
-                    else
-                        part[((wave * 3 + (x > wave ? x - 1 : x)) * JT + i) * kWave + lane] = v;
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const f32x4 v = room[(((y - 1) * L::RW + rw) * MT * 4 + 4 * i + x) * kWave + lane];
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) o[i][4 * x + z] += v[z];
                 }
-            __syncthreads();
-#pragma unroll
-            for (int w = 0; w < kDecWaves; ++w)
-                if (w != wave)
-#pragma unroll
-                    for (int i = 0; i < JT; ++i)
-                        mine[i] += part[((w * 3 + (wave > w ? wave - 1 : wave)) * JT + i) * kWave + lane];
-            if (live[n]) {  // register y of tile i: channel (8 wave + 4 hf + y) * MT + i
-                float *dst = a.po + at * DH + (8 * wave + 4 * hf) * MT + i0;
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    float v[JT];
-#pragma unroll
-                    for (int i = 0; i < JT; ++i) v[i] = __builtin_ldexpf(mine[i][y] * unshift, -dv);
-                    if constexpr (JT == 4)
-                        *(f32x4 *)(dst + y * MT) = f32x4{v[0], v[1], v[2], v[3]};
-                    else
-                        *(f32x2 *)(dst + y * MT) = f32x2{v[0], v[1]};
-                }
-            }
-        }
     }
+    if (!live) return;
+    const size_t at = ((size_t)t * a.H + h) * a.chunks + ci;
+    if (hf == 0) a.pml[at] = f32x2{__builtin_ldexpf(top, qexp - dk), l * unshift};
+    float *dst = a.po + at * DH + 4 * hf;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            f32x4 v;
+#pragma unroll
+            for (int z = 0; z < 4; ++z) v[z] = __builtin_ldexpf(o[i][4 * x + z] * keep, -dv);
+            *(f32x4 *)(dst + 32 * i + 8 * x) = v;
+        }
 }
 
-template <int TYPE, int DH, int NR>
-static int launch_prefix_nr(const DecodeArgs &a, hipStream_t stream) {
-    const long long rows = (long long)a.G * a.Tq * a.c.B, grid = (rows + 32 * NR - 1) / (32 * NR) * a.c.Hkv * a.prefix_chunks;
+template <int TYPE, int DH, int KS>
+static int launch_prefix_ks(const DecodeArgs &a, hipStream_t stream) {
+    constexpr int ROWS = PfxTile<DH, KS>::ROWS;
+    const long long rows = (long long)a.G * a.Tq * a.c.B, grid = (rows + ROWS - 1) / ROWS * a.c.Hkv * a.prefix_chunks;
     if (grid > kMaxGroups) return QG_ERR_SHAPE;
-    hipLaunchKernelGGL((attn_prefix_kernel<TYPE, DH, NR>), dim3((unsigned)grid), dim3(kDecWaves * kWave), 0, stream, a);
+    hipLaunchKernelGGL((attn_prefix_kernel<TYPE, DH, KS>), dim3((unsigned)grid), dim3(kDecWaves * kWave), 0, stream, a);
     return hipGetLastError() == hipSuccess ? QG_OK : QG_ERR_LAUNCH;
+}
+
+template <int TYPE, int DH>
+static int launch_prefix_dh(const DecodeArgs &a, hipStream_t stream) {
+    switch (prefix_tile_rows((long long)a.G * a.Tq * a.c.B, DH)) {
+        case 128: return launch_prefix_ks<TYPE, DH, 1>(a, stream);
+        case 64: return launch_prefix_ks<TYPE, DH, 2>(a, stream);
+        default: return launch_prefix_ks<TYPE, DH, DH == 256 ? 2 : 4>(a, stream);
+    }
 }
 
 template <int TYPE>
 static int launch_prefix(const DecodeArgs &a, int Dh, hipStream_t stream) {
-    const bool few = prefix_tile_rows((long long)a.G * a.Tq * a.c.B, Dh) == 32;
     switch (Dh) {
-        case 64: return few ? launch_prefix_nr<TYPE, 64, 1>(a, stream) : launch_prefix_nr<TYPE, 64, 2>(a, stream);
-        case 128: return few ? launch_prefix_nr<TYPE, 128, 1>(a, stream) : launch_prefix_nr<TYPE, 128, 2>(a, stream);
-        default: return launch_prefix_nr<TYPE, 256, 1>(a, stream);
+        case 64: return launch_prefix_dh<TYPE, 64>(a, stream);
+        case 128: return launch_prefix_dh<TYPE, 128>(a, stream);
+        default: return launch_prefix_dh<TYPE, 256>(a, stream);
     }
 }
 
-// Chunks that fill the card once, two workgroups a compute unit.
+// Chunks that fill the card once, as many workgroups a compute unit as fit.
 PrefixSplit prefix_split(long long rows, int Hkv, int Dh, int prefix) {
     const int tile = prefix_tile_rows(rows, Dh);
-    const long long groups = (rows + tile - 1) / tile * Hkv;
-    long long chunks = groups < 512 ? 512 / groups : 1;
+    const long long groups = (rows + tile - 1) / tile * Hkv, fit = Dh == 256 || tile == 32 ? 256 : 512;
+    const long long chunks = groups < fit ? fit / groups : 1;
     long long each = (prefix + chunks - 1) / chunks;
-    each = (each + kPfxStride - 1) / kPfxStride * kPfxStride;
+    each = (each + 127) / 128 * 128;
     if (each > kDecChunkMax) each = kDecChunkMax;
     return PrefixSplit{(int)each, (int)((prefix + each - 1) / each)};
 }

@@ -126,6 +126,15 @@ __device__ __forceinline__ int wave_find_last(int B, int x, F key) {
     return __builtin_amdgcn_readfirstlane(lo);
 }
 
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// Four rows of one column each, out of LDS.
+__device__ __forceinline__ u32x2 lds_read_column4(const char *p) {
+    const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) s16x4 *)const_cast<char *>(p));
+    return __builtin_bit_cast(u32x2, x);
+}
+
 // Maximum over the two lanes that hold one row (32 apart).
 __device__ __forceinline__ float half_max(float x) {
     const uint32_t u = __builtin_bit_cast(uint32_t, x);
