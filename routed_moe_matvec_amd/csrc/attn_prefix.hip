@@ -73,21 +73,33 @@ template <int DH, int KS>
 struct PfxTile {
     static constexpr int RW = kDecWaves / KS, ROWS = 32 * RW;
     static constexpr int N = KS == 4 || DH == 64 ? 128 : KS == 1 && DH == 256 ? 32 : 64;  // positions
-    static constexpr int CH = DH / 8, BYTES = N * DH * 2, PER = N * DH / 8192;               // 16-byte pieces that a thread loads of K, and of V
+    static constexpr int CH = DH / 8, BYTES = N * DH * 2;
+    static constexpr int PER = N * DH / 8192;                   // 16-byte pieces that a thread loads of K, and of V
+    static constexpr int STAGES = BYTES <= 16384 ? 2 : 1;       // so that two workgroups share a compute unit
     __device__ static int k_piece(int r, int p) { return p ^ (r & (CH < 16 ? CH - 1 : 15)); }
     __device__ static int v_piece(int r, int p) { return p ^ (DH == 64 ? (r >> 1 & 1) << 2 : (r & 3) << 2); }
 };
 
+template <int DH, int KS>
+struct PfxShared {
+    char stage[PfxTile<DH, KS>::STAGES][2][PfxTile<DH, KS>::BYTES];
+    f32x2 ml[KS][kDecWaves][32];
+    uint32_t bytes[2][kDecWaves];
+    int page[kDecChunkMax / 16];
+};
+
 template <int TYPE, int DH, int KS>
-__global__ __launch_bounds__(kDecWaves *kWave, DH == 256 || KS == 4 ? 1 : 2) void attn_prefix_kernel(DecodeArgs a) {
+__device__ __forceinline__ void attn_prefix_group(const DecodeArgs &a, PfxShared<DH, KS> &sh, const int id) {
     typedef typename ElemOf<TYPE>::type T;
     typedef PfxTile<DH, KS> L;
     constexpr int N = L::N, NT = N / 32 / KS, KC = DH / 16, MT = DH / 32, PER = L::PER;
     constexpr int QS = kQParts<TYPE>, QF = QS == 3 ? 2 : 1;  // parts of q in bf16 and in fp16
-    __shared__ __attribute__((aligned(16))) char stage[2][2][L::BYTES];
-    __shared__ f32x2 sml[KS][kDecWaves][32];
-    __shared__ uint32_t sbytes[2][kDecWaves];
-    __shared__ int spage[kDecChunkMax / 16];
+    auto &stage = sh.stage;
+    auto &sml = sh.ml;
+    auto &sbytes = sh.bytes;
+    auto &spage = sh.page;
+    Kv4Cache prefix = a.c;
+    prefix.pages = a.prefix_pages;
     const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int c = lane & 31, hf = lane >> 5, rw = wave % L::RW, ks = KS == 1 ? 0 : wave / L::RW;
 
@@ -95,7 +107,7 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 || KS == 4 ? 1 : 2) voi
     const int R = a.G * a.Tq * a.c.B, tiles = (R + L::ROWS - 1) / L::ROWS, units = a.c.Hkv * a.prefix_chunks;
     int u, rt;
     {
-        const int id = blockIdx.x, whole = units / 8 * 8 * tiles;
+        const int whole = units / 8 * 8 * tiles;
         if (id < whole) {
             rt = (id >> 3) % tiles;
             u = (id >> 3) / tiles * 8 + (id & 7);
@@ -111,9 +123,8 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 || KS == 4 ? 1 : 2) voi
 
     bool bad = false;
     for (int i = tid; i <= ((last - 1) >> a.c.page_log2) - pg0; i += kDecWaves * kWave) {
-        const int id = kv4_page_of(a.c, 0, pg0 + i);
-        spage[i] = id;
-        bad |= id < 0;
+        spage[i] = kv4_page_of(prefix, 0, pg0 + i);
+        bad |= spage[i] < 0;
     }
     // the lane's row, and what it sees
     const int row = rt * L::ROWS + 32 * rw + c;
@@ -389,18 +400,26 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 || KS == 4 ? 1 : 2) voi
             }
     };
     auto walk = [&](auto is_fast) {
-        store(first, stage[0][0], stage[0][1], is_fast);
-        if (first + N < last) load(first + N);
+        if constexpr (L::STAGES == 2) {
+            store(first, stage[0][0], stage[0][1], is_fast);
+            if (first + N < last) load(first + N);
+        }
         int s = 0;
         for (int j = first; j < last; j += N) {
             // this tile's operands are there for all waves, and all are done with the other stage
             lds_barrier();
-            if (j + N < last) {
-                store(j + N, stage[s ^ 1][0], stage[s ^ 1][1], is_fast);
-                if (j + 2 * N < last) load(j + 2 * N);
+            if constexpr (L::STAGES == 2) {
+                if (j + N < last) {
+                    store(j + N, stage[s ^ 1][0], stage[s ^ 1][1], is_fast);
+                    if (j + 2 * N < last) load(j + 2 * N);
+                }
+            } else {
+                store(j, stage[0][0], stage[0][1], is_fast);
+                if (j + N < last) load(j + N);
+                lds_barrier();
             }
             step(j, stage[s][0], stage[s][1], is_fast);
-            s ^= 1;
+            if (L::STAGES == 2) s ^= 1;
         }
     };
     if (fast)
@@ -461,18 +480,35 @@ __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 || KS == 4 ? 1 : 2) voi
         }
 }
 
+// The shared positions' workgroups, then those of the sequences' own positions, which
+// are shorter and fill what is left of the card.
+template <int TYPE, int DH, int KS>
+__global__ __launch_bounds__(kDecWaves *kWave, DH == 256 && TYPE == QG_TYPE_F32 ? 1 : 2) void attn_prefix_kernel(
+    DecodeArgs a, int shared_groups, int own_groups) {
+    constexpr size_t P = sizeof(PfxShared<DH, KS>), D = sizeof(DecShared<DH>);
+    __shared__ __attribute__((aligned(16))) char room[P > D ? P : D];
+    const int id = blockIdx.x;
+    if (id < shared_groups)
+        attn_prefix_group<TYPE, DH, KS>(a, *reinterpret_cast<PfxShared<DH, KS> *>(room), id);
+    else
+        attn_decode_group<TYPE, DH, 1, TAIL>(a, *reinterpret_cast<DecShared<DH> *>(room), (id - shared_groups) % own_groups,
+                                             (id - shared_groups) / own_groups);
+}
+
 template <int TYPE, int DH, int KS>
 static int launch_prefix_ks(const DecodeArgs &a, hipStream_t stream) {
     constexpr int ROWS = PfxTile<DH, KS>::ROWS;
-    const long long rows = (long long)a.G * a.Tq * a.c.B, grid = (rows + ROWS - 1) / ROWS * a.c.Hkv * a.prefix_chunks;
-    if (grid > kMaxGroups) return QG_ERR_SHAPE;
-    hipLaunchKernelGGL((attn_prefix_kernel<TYPE, DH, KS>), dim3((unsigned)grid), dim3(kDecWaves * kWave), 0, stream, a);
+    const long long rows = (long long)a.G * a.Tq * a.c.B, shared = (rows + ROWS - 1) / ROWS * a.c.Hkv * a.prefix_chunks;
+    const long long own = (long long)a.c.Hkv * a.c.B * (a.chunks - a.prefix_chunks), tiles = (a.G * a.Tq + 15) / 16;
+    if (shared + own * tiles > kMaxGroups) return QG_ERR_SHAPE;
+    hipLaunchKernelGGL((attn_prefix_kernel<TYPE, DH, KS>), dim3((unsigned)(shared + own * tiles)),
+                       dim3(kDecWaves * kWave), 0, stream, a, (int)shared, (int)own);
     return hipGetLastError() == hipSuccess ? QG_OK : QG_ERR_LAUNCH;
 }
 
 template <int TYPE, int DH>
 static int launch_prefix_dh(const DecodeArgs &a, hipStream_t stream) {
-    switch (prefix_tile_rows((long long)a.G * a.Tq * a.c.B, DH)) {
+    switch (a.prefix_rows) {
         case 128: return launch_prefix_ks<TYPE, DH, 1>(a, stream);
         case 64: return launch_prefix_ks<TYPE, DH, 2>(a, stream);
         default: return launch_prefix_ks<TYPE, DH, DH == 256 ? 2 : 4>(a, stream);
@@ -488,15 +524,32 @@ static int launch_prefix(const DecodeArgs &a, int Dh, hipStream_t stream) {
     }
 }
 
-// Chunks that fill the card once, as many workgroups a compute unit as fit.
-PrefixSplit prefix_split(long long rows, int Hkv, int Dh, int prefix) {
-    const int tile = prefix_tile_rows(rows, Dh);
-    const long long groups = (rows + tile - 1) / tile * Hkv, fit = Dh == 256 || tile == 32 ? 256 : 512;
-    const long long chunks = groups < fit ? fit / groups : 1;
-    long long each = (prefix + chunks - 1) / chunks;
-    each = (each + 127) / 128 * 128;
-    if (each > kDecChunkMax) each = kDecChunkMax;
-    return PrefixSplit{(int)each, (int)((prefix + each - 1) / each)};
+// Rows of a workgroup and chunks that take the least time by what was measured (us, fp32
+// queries, 128 channels): 128 positions of 128, 64, 32 rows take a workgroup 5.2, 2.5, 1.5 alone
+// on a compute unit, 7.4, 4.2, 2.5 beside another; a second one leaves no room for the sequences' own
+// positions, which then come behind (8); a chunk's sums, written and read, 0.4 a megabyte.  48
+// sequences of 8 rows a head over 40001: 128 rows in 21 chunks 128, in 11 168, 64 rows 145, 32
+// rows 173; 32 of 4 rows over 6001: 128 rows in 32 chunks 27, 64 in 16 26, 32 in 8 24, in 16 31.
+// Each sequence by itself (no chunks) takes about 22 for 10^6 times 16 rows' positions, and
+// 3 less to begin with: 4 sequences over 300 8.4 and 13.9, 2 over 30000 20 and 28, 48 of 16 rows
+// over 1500 28 and 34, 16 of 4 rows over 4000 22 and 18, 8 of 2 over 16000 27 and 18.
+PrefixSplit prefix_split(int B, long long rows, int Hkv, int Dh, int prefix) {
+    PrefixSplit best{0, 0, 0};
+    double least = (double)((rows / B + 15) / 16) * B * Hkv * prefix * Dh / 128 * 22e-6 - 3;
+    for (int tile = 128; tile >= (Dh == 256 ? 64 : 32); tile /= 2)
+        for (int fit = 256; fit <= 512; fit *= 2) {
+            const long long groups = (rows + tile - 1) / tile * Hkv;
+            long long chunks = groups < fit ? fit / groups : 1;
+            long long each = ((prefix + chunks - 1) / chunks + 127) / 128 * 128;
+            if (each > kDecChunkMax) each = kDecChunkMax;
+            chunks = (prefix + each - 1) / each;
+            const bool beside = groups * chunks > 256;
+            const double step = tile == 128 ? (beside ? 7.4 : 5.2) : tile == 64 ? (beside ? 4.2 : 2.5) : beside ? 2.5 : 1.5;
+            const double rounds = (double)((groups * chunks + 511) / 512);
+            const double us = rounds * each / 128 * step * Dh / 128 + (beside ? 8 : 0) + rows * Hkv * chunks * Dh * 4 * 0.4e-6;
+            if (us < least) best = PrefixSplit{tile, (int)each, (int)chunks}, least = us;
+        }
+    return best;
 }
 
 int launch_attn_prefix(int type, int Dh, const DecodeArgs &a, hipStream_t stream) {
