@@ -24,10 +24,10 @@
 
 namespace qg {
 
-template <int TYPE, int DH, int SLOTS, int MODE>
-__global__ __launch_bounds__(kDecWaves *kWave, DH == 256 ? 3 : 4) void attn_decode_kernel(DecodeArgs a) {
-    __shared__ DecShared<DH> sh;
-    attn_decode_group<TYPE, DH, SLOTS, MODE>(a, sh, blockIdx.x, blockIdx.y);
+template <int TYPE, int DH, int SLOTS, int MODE, int WAVES>
+__global__ __launch_bounds__(WAVES *kWave, DH == 256 ? 3 : 4) void attn_decode_kernel(DecodeArgs a) {
+    __shared__ DecShared<DH, WAVES> sh;
+    attn_decode_group<TYPE, DH, SLOTS, MODE, WAVES>(a, sh, blockIdx.x, blockIdx.y);
 }
 
 // Joins the chunks of sequences that have several: one workgroup per query
@@ -88,15 +88,15 @@ __global__ __launch_bounds__(256) void attn_decode_join_kernel(DecodeArgs a) {
     *(f32x4 *)(a.y + ((size_t)b * rows + row) * DH + ch * 4) = acc * (l > 0.f ? 1.f / l : 0.f);
 }
 
-template <int TYPE, int DH, int MODE>
-static int launch_decode_mode(const DecodeArgs &a, int chunks, hipStream_t stream) {
+template <int TYPE, int DH, int MODE, int WAVES = kDecWaves>
+static int launch_decode_mode(const DecodeArgs &a, hipStream_t stream) {
     constexpr int SLOTS = kQParts<TYPE> == 3 ? 2 : 1;
     const int rows = a.G * a.Tq;
-    const dim3 grid((unsigned)((long long)a.c.Hkv * a.c.B * chunks), (rows + 15) / 16), block(kDecWaves * kWave);
+    const dim3 grid((unsigned)((long long)a.c.Hkv * a.c.B * a.chunks), (rows + 15) / 16), block(WAVES * kWave);
     if (rows <= 16 / SLOTS)
-        hipLaunchKernelGGL((attn_decode_kernel<TYPE, DH, SLOTS, MODE>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((attn_decode_kernel<TYPE, DH, SLOTS, MODE, WAVES>), grid, block, 0, stream, a);
     else
-        hipLaunchKernelGGL((attn_decode_kernel<TYPE, DH, 1, MODE>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((attn_decode_kernel<TYPE, DH, 1, MODE, WAVES>), grid, block, 0, stream, a);
     return hipGetLastError() == hipSuccess ? QG_OK : QG_ERR_LAUNCH;
 }
 
@@ -112,13 +112,15 @@ static int launch_decode_dh(const DecodeArgs &a, hipStream_t stream) {
         const int rc = launch_attn_prefix(TYPE, DH, a, stream);
         return rc == QG_OK ? launch_join<DH, TAIL>(a, stream) : rc;
     }
-    if (a.prefix) {
-        const int rc = launch_decode_mode<TYPE, DH, FUSED>(a, a.chunks, stream);
-        return rc != QG_OK || a.chunks == 1 ? rc : launch_join<DH, FUSED>(a, stream);
-    }
-    const int rc = a.sinks ? launch_decode_mode<TYPE, DH, SINKS>(a, a.chunks, stream)
-                           : launch_decode_mode<TYPE, DH, PLAIN>(a, a.chunks, stream);
+    int rc;
+    if constexpr (DH <= 128)
+        if (a.wide) return a.prefix ? launch_decode_mode<TYPE, DH, FUSED, 8>(a, stream) : launch_decode_mode<TYPE, DH, SINKS, 8>(a, stream);
+    if (a.prefix)
+        rc = launch_decode_mode<TYPE, DH, FUSED>(a, stream);
+    else
+        rc = a.sinks ? launch_decode_mode<TYPE, DH, SINKS>(a, stream) : launch_decode_mode<TYPE, DH, PLAIN>(a, stream);
     if (rc != QG_OK || a.chunks == 1) return rc;
+    if (a.prefix) return launch_join<DH, FUSED>(a, stream);
     return a.sinks ? launch_join<DH, SINKS>(a, stream) : launch_join<DH, PLAIN>(a, stream);
 }
 
@@ -135,19 +137,31 @@ static int launch_decode(const DecodeArgs &a, int Dh, hipStream_t stream) {
 struct DecodeChunks {
     PrefixSplit prefix;  // no chunks: each sequence walks it by itself
     DecSplit own;
-    int all;  // chunks of the prefix and a sequence
+    bool wide;  // one chunk, of eight waves
+    int all;    // chunks of the prefix and a sequence
 };
+// With two ranges of up to 1280 positions of 128 channels a sequence is one chunk, which eight waves
+// share: no join.  us with that, and with chunks of four waves: 1024 positions and 4 sinks of 1, 16, 32,
+// 64 sequences with 8 key heads 9.9, 10.4, 11.5, 18.5 and 8.8, 11.6, 16.7, 26; 2048 15, 16, 17.5,
+// 29 and 10.5, 14.6, 21.9, 35; 500 7.8, 7.9, 8.3, 12.3 and 8.7, 8.8, 9.1, 12.2.  A rule of the call's
+// window and sinks: a sequence's result does not depend on max_len.
 static DecodeChunks decode_chunks(int B, int Tq, int G, int Hkv, int Dh, int max_len, int window, int sinks, int prefix) {
-    DecodeChunks n{{0, 0, 0}, dec_split(G * Tq, Dh), 0};
-    long long most = max_len;
+    DecodeChunks n{{0, 0, 0}, dec_split(G * Tq, Dh), false, 0};
+    long long most = max_len, two = 1LL << 40;
     if (prefix) n.prefix = prefix_split(B, (long long)B * Tq * G, Hkv, Dh, prefix);
     if (n.prefix.chunks) {
         n.own.least = 11 + 7 - n.own.dh_log2;
         most = max_len > prefix ? max_len - (prefix & ~15) : 0;
     } else if (prefix) {
-        most = max_len + 16LL;
-    } else if (window && (long long)window + Tq - 1 + 15 + (sinks + 15LL) / 16 * 16 < most) {
-        most = (long long)window + Tq - 1 + 15 + (sinks + 15LL) / 16 * 16;
+        most = two = max_len + 16LL;
+    } else if (window) {
+        const long long held = (long long)window + Tq - 1 + 15 + (sinks + 15LL) / 16 * 16;
+        if (sinks) two = held;
+        if (held < most) most = held;
+    }
+    if (two * Dh <= 1280 * 128 && Dh <= 128) {
+        n.wide = true;
+        n.own.least = 13;
     }
     n.all = n.prefix.chunks + (most ? n.own.chunks_max((int)most) : 0);
     return n;
@@ -210,6 +224,7 @@ static int decode(int type, const void *q, int ldq, const int32_t *lens, int B, 
     a.qsign = scale > 0.f ? 1.f : scale < 0.f ? -1.f : 0.f;
     const DecodeChunks n = decode_chunks(B, Tq, a.G, Hkv, Dh, max_len, window, sinks, prefix);
     a.chunks = n.all;
+    a.wide = n.wide;
     a.prefix_chunks = n.prefix.chunks;
     a.prefix_each = n.prefix.each;
     a.prefix_rows = n.prefix.rows;

@@ -69,6 +69,7 @@ struct DecodeArgs {
     int sinks;
     int prefix, prefix_each, prefix_chunks;  // positions, those of a chunk, and the chunks (0: FUSED)
     int prefix_rows;
+    bool wide;  // one chunk, of eight waves
     const int32_t *prefix_pages;
     float scale;  // times log2(e), not negative
     float qsign;  // 1, -1 (a negative scale) or 0 (scale 0)
@@ -249,27 +250,27 @@ __device__ __forceinline__ float across8(float x) {
 // rows a head, 40.1 -> 37.8 us.  With one or two parts of the queries, and only the
 // weights to gain on, it did not: 32 sequences of 4 rows in bf16 18.6 -> 18.9 us, of
 // 2 rows in fp16 34.6 -> 34.9.
-template <int DH>
+template <int DH, int WAVES>
 struct DecShared {
     static constexpr int PER = DH == 64 ? 4 : 8;  // channel tiles joined at a time
-    f32x4 sums[kDecWaves * PER * kWave];
-    f32x2 ml[kDecWaves][16];
+    f32x4 sums[WAVES * PER * kWave];
+    f32x2 ml[WAVES][16];
     int page[kDecChunkMax / 16 + 2];
 };
 
 // One workgroup: chunk group / (B Hkv) of a sequence and key/value head, rows from tile * 16 / SLOTS on.
-template <int TYPE, int DH, int SLOTS, int MODE>
-__device__ __forceinline__ void attn_decode_group(const DecodeArgs &a, DecShared<DH> &sh, const int group, const int tile) {
+template <int TYPE, int DH, int SLOTS, int MODE, int WAVES>
+__device__ __forceinline__ void attn_decode_group(const DecodeArgs &a, DecShared<DH, WAVES> &sh, const int group, const int tile) {
     typedef typename ElemOf<TYPE>::type T;
     constexpr int QP = kQParts<TYPE>, KC = DH / 32, MT = DH / 16;  // parts of q, key products, channel tiles
     constexpr int ROWS = 16 / SLOTS, QO = (QP + SLOTS - 1) / SLOTS, PO = (3 + SLOTS - 1) / SLOTS;  // operands
     // queries of more than 16 registers stay in LDS, in the room that the join uses at the end: more waves fit
     constexpr bool QLDS = QO * KC > 4;
-    constexpr int PER = DecShared<DH>::PER;
-    f32x4(&so)[kDecWaves * PER * kWave] = sh.sums;
+    constexpr int PER = DecShared<DH, WAVES>::PER;
+    f32x4(&so)[WAVES * PER * kWave] = sh.sums;
     u32x4 *sq = reinterpret_cast<u32x4 *>(&so[0]);
     static_assert(!QLDS || sizeof(so) >= sizeof(u32x4) * QO * KC * kWave, "queries fit the join's room");
-    f32x2(&sml)[kDecWaves][16] = sh.ml;
+    f32x2(&sml)[WAVES][16] = sh.ml;
     int(&spage)[kDecChunkMax / 16 + 2] = sh.page;
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     // sequence by sequence within a chunk number: the workgroups of chunks that a
@@ -293,13 +294,13 @@ __device__ __forceinline__ void attn_decode_group(const DecodeArgs &a, DecShared
 
     // queries as the B operand: column c, for product i channels 8 i + 0..7 of the
     // lane's (16 g.. of 64, 32 g.. of each 128); requested first, used once the first keys are on their way
-    constexpr int QN = QLDS ? (KC + kDecWaves - 1) / kDecWaves : KC;
+    constexpr int QN = QLDS ? (KC + WAVES - 1) / WAVES : KC;
     Raw8<T> qraw[QN];
     {
         const T *qp = (const T *)a.q + (size_t)(b * a.Tq + t) * a.ldq + (size_t)h * DH + g * (DH == 64 ? 16 : 32);
 #pragma unroll
         for (int i = 0; i < QN; ++i) {
-            const int at = QLDS ? min(i * kDecWaves + wave, KC - 1) : i;
+            const int at = QLDS ? min(i * WAVES + wave, KC - 1) : i;
             qraw[i] = load8(qp + at / 4 * 128 + at % 4 * 8);
         }
     }
@@ -337,7 +338,7 @@ __device__ __forceinline__ void attn_decode_group(const DecodeArgs &a, DecShared
     const int n_sink = TWO && first < r.edge ? ((min(last, r.edge) - 1) >> a.c.page_log2) - pg_sink + 1 : 0;
     const int pg0 = ((TWO ? max(first, r.edge) : first) + r.gap) >> a.c.page_log2;
     const int n_pages = TWO && last <= r.edge ? n_sink : n_sink + ((last - 1 + r.gap) >> a.c.page_log2) - pg0 + 1;
-    for (int i = threadIdx.x; i < n_pages; i += kDecWaves * kWave)
+    for (int i = threadIdx.x; i < n_pages; i += WAVES * kWave)
         spage[i] = MODE == FUSED && i < n_sink ? kv4_page_of(prefix, 0, pg_sink + i)
                                                : kv4_page_of(a.c, b, i < n_sink ? pg_sink + i : pg0 + i - n_sink);
     __syncthreads();
@@ -370,7 +371,7 @@ __device__ __forceinline__ void attn_decode_group(const DecodeArgs &a, DecShared
         for (int x = 0; x < 2; ++x) dec_load_v<DH>(cur[x], at_region[x], page, at_off[x], ln);
         stay();
     };
-    constexpr int kStride = kDecWaves * kDecStep;
+    constexpr int kStride = WAVES * kDecStep;
     const int j_first = first + wave * kDecStep;
     locate(j_first);
     load_k();
@@ -379,7 +380,7 @@ __device__ __forceinline__ void attn_decode_group(const DecodeArgs &a, DecShared
     u32x4 qf[QO][QLDS ? 1 : KC];
 #pragma unroll
     for (int i = 0; i < QN; ++i) {
-        const int at = QLDS ? i * kDecWaves + wave : i;
+        const int at = QLDS ? i * WAVES + wave : i;
         bf16x8 parts[QP];
         split8<QP>(qraw[i], a.qsign, parts);
 #pragma unroll
@@ -556,9 +557,9 @@ __device__ __forceinline__ void attn_decode_group(const DecodeArgs &a, DecShared
     auto joined = [&](int r) {  // maximum and sum of a row
         float top = -INFINITY, sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < kDecWaves; ++w) top = __builtin_fmaxf(top, sml[w][r][0]);
+        for (int w = 0; w < WAVES; ++w) top = __builtin_fmaxf(top, sml[w][r][0]);
 #pragma unroll
-        for (int w = 0; w < kDecWaves; ++w)
+        for (int w = 0; w < WAVES; ++w)
             sum += sml[w][r][1] * __builtin_amdgcn_exp2f((sml[w][r][0] - (top == -INFINITY ? 0.f : top)) * a.scale);
         return f32x2{top, sum};
     };
@@ -569,6 +570,7 @@ __device__ __forceinline__ void attn_decode_group(const DecodeArgs &a, DecShared
     constexpr int PART = PER / SLOTS;
     const int wk = threadIdx.x & 3, wc = (threadIdx.x >> 2) % ROWS, wg = threadIdx.x >> 6;
     const int wi = (threadIdx.x >> 2) % 16 / ROWS * PART;
+    const bool adds = WAVES == 4 || threadIdx.x < 256;
     const int wrow = row0 + wc;
     const int wt = token_of(wrow);
     const size_t wout = (size_t)(b * a.Tq + wt) * a.H + hk * a.G + wrow - wt * a.G;
@@ -579,7 +581,7 @@ __device__ __forceinline__ void attn_decode_group(const DecodeArgs &a, DecShared
         const int chunk = MODE == TAIL ? a.prefix_chunks + ci : ci;
         dst = a.po + (wout * a.chunks + chunk) * DH;
         f = 1.f;
-        if (wrow < R && wg == 0 && wk == 0 && wi == 0) a.pml[wout * a.chunks + chunk] = ml;
+        if (adds && wrow < R && wg == 0 && wk == 0 && wi == 0) a.pml[wout * a.chunks + chunk] = ml;
     }
 #pragma unroll
     for (int y = 0; y < DecTile<DH>::VC; ++y) {
@@ -587,12 +589,13 @@ __device__ __forceinline__ void attn_decode_group(const DecodeArgs &a, DecShared
 #pragma unroll
         for (int i = 0; i < PER; ++i) so[(wave * PER + i) * kWave + lane] = o[8 * y + i] * keep;
         __syncthreads();
+        if (!adds) continue;
         float acc[PART];
 #pragma unroll
         for (int i = 0; i < PART; ++i) {
             acc[i] = 0.f;
 #pragma unroll
-            for (int w = 0; w < kDecWaves; ++w)
+            for (int w = 0; w < WAVES; ++w)
 #pragma unroll
                 for (int x = 0; x < SLOTS; ++x)
                     acc[i] += reinterpret_cast<const float *>(

@@ -485,13 +485,13 @@ __device__ __forceinline__ void attn_prefix_group(const DecodeArgs &a, PfxShared
 template <int TYPE, int DH, int KS>
 __global__ __launch_bounds__(kDecWaves *kWave, DH == 256 && TYPE == QG_TYPE_F32 ? 1 : 2) void attn_prefix_kernel(
     DecodeArgs a, int shared_groups, int own_groups) {
-    constexpr size_t P = sizeof(PfxShared<DH, KS>), D = sizeof(DecShared<DH>);
+    constexpr size_t P = sizeof(PfxShared<DH, KS>), D = sizeof(DecShared<DH, kDecWaves>);
     __shared__ __attribute__((aligned(16))) char room[P > D ? P : D];
     const int id = blockIdx.x;
     if (id < shared_groups)
         attn_prefix_group<TYPE, DH, KS>(a, *reinterpret_cast<PfxShared<DH, KS> *>(room), id);
     else
-        attn_decode_group<TYPE, DH, 1, TAIL>(a, *reinterpret_cast<DecShared<DH> *>(room), (id - shared_groups) % own_groups,
+        attn_decode_group<TYPE, DH, 1, TAIL, kDecWaves>(a, *reinterpret_cast<DecShared<DH, kDecWaves> *>(room), (id - shared_groups) % own_groups,
                                              (id - shared_groups) / own_groups);
 }
 
