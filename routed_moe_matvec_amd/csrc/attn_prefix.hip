@@ -48,25 +48,34 @@ struct PfxOps {
 
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
-// Least and largest of the scale bytes seen so far, in the halves of two dwords.
+// Of the scale bytes seen so far the largest, and 255 less the least, both twice (in the halves).
 struct ByteRange {
-    u16x2 lo = {255, 255}, hi = {0, 0};
+    u16x2 hi = {0, 0}, lo = {0, 0};
     __device__ void add(uint32_t w) {
-        const u16x2 e = __builtin_bit_cast(u16x2, w & 0x00ff00ffu), o = __builtin_bit_cast(u16x2, (w >> 8) & 0x00ff00ffu);
-        lo = __builtin_elementwise_min(lo, __builtin_elementwise_min(e, o));
-        hi = __builtin_elementwise_max(hi, __builtin_elementwise_max(e, o));
+        const uint32_t n = ~w;
+        auto top = [](uint32_t x) {
+            return __builtin_elementwise_max(__builtin_bit_cast(u16x2, x & 0x00ff00ffu), __builtin_bit_cast(u16x2, (x >> 8) & 0x00ff00ffu));
+        };
+        hi = __builtin_elementwise_max(hi, top(w));
+        lo = __builtin_elementwise_max(lo, top(n));
     }
-    // least and largest of the wave's bytes, as least + 256 * largest
-    __device__ uint32_t of_wave() const {
-        int l = min((int)lo[0], (int)lo[1]), h = max((int)hi[0], (int)hi[1]);
-#pragma unroll
-        for (int x = 1; x < kWave; x <<= 1) {
-            l = min(l, shfl_xor(l, x));
-            h = max(h, shfl_xor(h, x));
-        }
-        return (uint32_t)(l | h << 8);
-    }
+    __device__ u16x2 both() const { return u16x2{hi[0] > hi[1] ? hi[0] : hi[1], lo[0] > lo[1] ? lo[0] : lo[1]}; }
 };
+
+// Maxima over the wave of two numbers a lane, in the last lane.
+__device__ __forceinline__ u16x2 wave_max2(u16x2 x) {
+#define QG_DPP_MAX(ctrl, rows)                                                                                   \
+    x = __builtin_elementwise_max(                                                                               \
+        x, __builtin_bit_cast(u16x2, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), ctrl, rows, 0xf, false)))
+    QG_DPP_MAX(0x111, 0xf);  // lane shifts by 1, 2, 4, 8 within rows of 16
+    QG_DPP_MAX(0x112, 0xf);
+    QG_DPP_MAX(0x114, 0xf);
+    QG_DPP_MAX(0x118, 0xf);
+    QG_DPP_MAX(0x142, 0xa);  // lane 15 of a row to the next
+    QG_DPP_MAX(0x143, 0xc);  // lane 31 to the upper half
+#undef QG_DPP_MAX
+    return x;
+}
 
 // A workgroup's shape: KS waves share 32 rows, each with its own positions of a tile.
 template <int DH, int KS>
@@ -84,7 +93,8 @@ template <int DH, int KS>
 struct PfxShared {
     char stage[PfxTile<DH, KS>::STAGES][2][PfxTile<DH, KS>::BYTES];
     f32x2 ml[KS][kDecWaves][32];
-    uint32_t bytes[2][kDecWaves];
+    u16x2 bytes[2][kDecWaves];  // of the chunk's key and value scales: the largest, and 255 less the least
+    int bad[kDecWaves], wide[kDecWaves];
     int page[kDecChunkMax / 16];
 };
 
@@ -126,6 +136,8 @@ __device__ __forceinline__ void attn_prefix_group(const DecodeArgs &a, PfxShared
         spage[i] = kv4_page_of(prefix, 0, pg0 + i);
         bad |= spage[i] < 0;
     }
+    const bool wave_bad = __ballot(bad) != 0;
+    if (lane == 0) sh.bad[wave] = wave_bad;
     // the lane's row, and what it sees
     const int row = rt * L::ROWS + 32 * rw + c;
     const bool live = row < R;
@@ -135,11 +147,16 @@ __device__ __forceinline__ void attn_prefix_group(const DecodeArgs &a, PfxShared
 #pragma unroll
     for (int i = 0; i < KC; ++i) qraw[i] = load8(qp + 16 * i);
     const int see_hi = live && len >= 0 && len <= a.max_len ? max(min(len - a.Tq + t % a.Tq + 1, last), 0) : 0;
-    int all_hi = live ? see_hi : last;
+    int all_hi = live ? see_hi : last;  // where what all of the wave's rows see ends
+    if (__ballot(all_hi != last))
 #pragma unroll
-    for (int x = 1; x < 32; x <<= 1) all_hi = min(all_hi, shfl_xor(all_hi, x));
+        for (int x = 1; x < 32; x <<= 1) all_hi = min(all_hi, shfl_xor(all_hi, x));
     all_hi = __builtin_amdgcn_readfirstlane(all_hi);
-    const bool any_bad = __syncthreads_or(bad);
+    lds_barrier();
+    bool any_bad = false;
+#pragma unroll
+    for (int w = 0; w < kDecWaves; ++w) any_bad |= sh.bad[w] != 0;
+    any_bad = __builtin_amdgcn_readfirstlane(any_bad);
 
     // A tile's bytes: keys by 32 channels of a position, values by 8 channels of four.  What lies
     // behind the end or on a bad page is read at the chunk's first place, or page 0, and has the scale 0.
@@ -222,70 +239,70 @@ __device__ __forceinline__ void attn_prefix_group(const DecodeArgs &a, PfxShared
                         r.add((w[d] >> (8 * b) & 255u) * 0x01010101u);
             }
         }
-        const uint32_t kr = k.of_wave(), vr = v.of_wave();
-        if (lane == 0) sbytes[0][wave] = kr, sbytes[1][wave] = vr;
+        const u16x2 kr = wave_max2(k.both()), vr = wave_max2(v.both());
+        if (lane == kWave - 1) sbytes[0][wave] = kr, sbytes[1][wave] = vr;
     }
-    float most_q = 0.f, least_q = INFINITY;  // of the row
+    int qexp = 0;  // power of two off the row's queries
     if constexpr (TYPE == QG_TYPE_F32) {
+        uint32_t most_q = 0, least_q = ~0u;  // magnitudes, as bits; the least that is not 0, less 1
 #pragma unroll
         for (int i = 0; i < KC; ++i)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float x = __builtin_fabsf(elem(qraw[i], e) * a.qsign);
-                most_q = __builtin_fmaxf(most_q, x);
-                least_q = __builtin_fminf(least_q, x > 0.f ? x : INFINITY);
+                const uint32_t x = __builtin_bit_cast(uint32_t, elem(qraw[i], e)) & 0x7fffffffu;
+                most_q = max(most_q, x);
+                least_q = min(least_q, x - 1);
             }
-        most_q = half_max(most_q);
-        least_q = -half_max(-least_q);
+        const float most = half_max(__builtin_bit_cast(float, most_q));
+        const float least = least_q == ~0u ? INFINITY : __builtin_bit_cast(float, least_q + 1);
+        if (most > 0.f) qexp = __builtin_amdgcn_frexp_expf(most) - 15;
+        // two parts hold 24 bits of what is within 2^26 of the row's largest
+        const bool wide = __ballot(least * 0x1p26f < most || qexp < -60 || qexp > 60) != 0;
+        if (lane == 0) sh.wide[wave] = wide;
     }
-    int qexp = 0;  // power of two off the row's queries
     bool fast;
     {
-        const int qe = most_q > 0.f ? __builtin_amdgcn_frexp_expf(most_q) - 15 : 0;
-        bool wide = TYPE == QG_TYPE_F32 && least_q * 0x1p26f < most_q;
         lds_barrier();  // the first tile's loads stay in flight
-        int kl = 255, kh = 0, vl = 255, vh = 0;
+        u16x2 k = {0, 0}, v = {0, 0};
+        fast = true;
 #pragma unroll
         for (int w = 0; w < kDecWaves; ++w) {
-            kl = min(kl, (int)(sbytes[0][w] & 255u)), kh = max(kh, (int)(sbytes[0][w] >> 8));
-            vl = min(vl, (int)(sbytes[1][w] & 255u)), vh = max(vh, (int)(sbytes[1][w] >> 8));
+            k = __builtin_elementwise_max(k, sbytes[0][w]);
+            v = __builtin_elementwise_max(v, sbytes[1][w]);
+            if (TYPE == QG_TYPE_F32) fast = fast && !sh.wide[w];
         }
         // the largest becomes 2^13 (6 * 2^13 < 65504), the least 2^-23 (half of it is fp16's least)
-        fast = vh - vl <= 36 && vh > 0;
-        dv = 140 - vh;
+        fast = fast && v[0] + v[1] <= 255 + 36 && v[0] > 0;
+        dv = 140 - v[0];
         if (TYPE != QG_TYPE_BF16) {
-            fast = fast && kh - kl <= 36 && kh > 0;
-            dk = 140 - kh;
+            fast = fast && k[0] + k[1] <= 255 + 36 && k[0] > 0;
+            dk = 140 - k[0];
         }
-        const int e = __builtin_amdgcn_frexp_expf(a.scale) + qe - dk;
-        wide |= e < -100 || e > 100;
-        fast = !__syncthreads_or(wide || !fast);
-        qexp = fast ? qe : 0;
+        const int e = __builtin_amdgcn_frexp_expf(a.scale) - dk;  // scores' factor, but for qexp: far from fp32's ends
+        fast = __builtin_amdgcn_readfirstlane(fast && e >= -60 && e <= 60);
         dk = __builtin_amdgcn_readfirstlane(fast ? dk : 0);
         dv = __builtin_amdgcn_readfirstlane(fast ? dv : 0);
+        if (!fast) qexp = 0;
     }
     const float scale = __builtin_ldexpf(a.scale, qexp - dk);  // of a row's scores as they are computed
 
     u32x4 qf[QF][KC];
+    if constexpr (TYPE == QG_TYPE_F32) {
+        const float factor = a.qsign * __builtin_ldexpf(1.f, -qexp);
 #pragma unroll
-    for (int i = 0; i < KC; ++i) {
-        if constexpr (TYPE == QG_TYPE_BF16) {
-            bf16x8 part[1];
-            split8<1>(qraw[i], a.qsign, part);
-            qf[0][i] = __builtin_bit_cast(u32x4, part[0]);
-        } else {
+        for (int i = 0; i < KC; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float x0 = __builtin_ldexpf(elem(qraw[i], 2 * e) * a.qsign, -qexp);
-                const float x1 = __builtin_ldexpf(elem(qraw[i], 2 * e + 1) * a.qsign, -qexp);
+                const float x0 = elem(qraw[i], 2 * e) * factor, x1 = elem(qraw[i], 2 * e + 1) * factor;
                 const f16x2 hi = __builtin_convertvector((f32x2{x0, x1}), f16x2);
+                const f32x2 rest = {__builtin_fmaf((float)hi[0], -1.f, x0), __builtin_fmaf((float)hi[1], -1.f, x1)};
                 qf[0][i][e] = __builtin_bit_cast(uint32_t, hi);
-                if constexpr (QF == 2) {
-                    const f32x2 rest = {x0 - (float)hi[0], x1 - (float)hi[1]};
-                    qf[1][i][e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest, f16x2));
-                }
+                qf[1][i][e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest, f16x2));
             }
-        }
+    } else {
+        const uint32_t flip = a.qsign < 0.f ? 0x80008000u : 0u, keep = a.qsign == 0.f ? 0u : ~0u;
+#pragma unroll
+        for (int i = 0; i < KC; ++i) qf[0][i] = (qraw[i].w[0] ^ flip) & keep;
     }
 
     f32x16 o[MT];
@@ -400,26 +417,25 @@ __device__ __forceinline__ void attn_prefix_group(const DecodeArgs &a, PfxShared
             }
     };
     auto walk = [&](auto is_fast) {
-        if constexpr (L::STAGES == 2) {
-            store(first, stage[0][0], stage[0][1], is_fast);
-            if (first + N < last) load(first + N);
-        }
-        int s = 0;
-        for (int j = first; j < last; j += N) {
-            // this tile's operands are there for all waves, and all are done with the other stage
-            lds_barrier();
-            if constexpr (L::STAGES == 2) {
+        if constexpr (L::STAGES == 2) {  // a tile's operands are made while the last one's are used
+            int s = 1;
+            for (int j = first - N; j < last; j += N) {
+                lds_barrier();  // all are done with the stage, and the other one is complete
                 if (j + N < last) {
                     store(j + N, stage[s ^ 1][0], stage[s ^ 1][1], is_fast);
                     if (j + 2 * N < last) load(j + 2 * N);
                 }
-            } else {
+                if (j >= first) step(j, stage[s][0], stage[s][1], is_fast);
+                s ^= 1;
+            }
+        } else {
+            for (int j = first; j < last; j += N) {
+                lds_barrier();
                 store(j, stage[0][0], stage[0][1], is_fast);
                 if (j + N < last) load(j + N);
                 lds_barrier();
+                step(j, stage[0][0], stage[0][1], is_fast);
             }
-            step(j, stage[s][0], stage[s][1], is_fast);
-            if (L::STAGES == 2) s ^= 1;
         }
     };
     if (fast)
@@ -430,9 +446,9 @@ __device__ __forceinline__ void attn_prefix_group(const DecodeArgs &a, PfxShared
     const float exact = most.exact(scale, fast ? 11.f : 0.f), unshift = fast ? 0x1p-11f : 1.f;
     float top = most.m, keep = exact * unshift;
     l = (l + shfl_xor(l, 32)) * exact;
-    if constexpr (KS > 1) {  // join the waves that share rows, through the stages
+    if constexpr (KS > 1) {  // maximum and sum of the waves that share rows
         if (hf == 0) sml[ks][rw][c] = f32x2{most.m, l};
-        __syncthreads();
+        __syncthreads();  // and all are done with the stages
         float sum = 0.f;
 #pragma unroll
         for (int x = 0; x < KS; ++x) top = __builtin_fmaxf(top, sml[x][rw][c][0]);
@@ -441,43 +457,45 @@ __device__ __forceinline__ void attn_prefix_group(const DecodeArgs &a, PfxShared
         for (int x = 0; x < KS; ++x) sum += sml[x][rw][c][1] * __builtin_amdgcn_exp2f((sml[x][rw][c][0] - use) * scale);
         keep *= __builtin_amdgcn_exp2f((most.m - use) * scale);
         l = sum;
-        static_assert(sizeof(stage) >= (KS - 1) * L::RW * 32 * DH * 4, "the waves' sums fit the stages");
-        f32x4 *room = reinterpret_cast<f32x4 *>(&stage[0][0][0]);
+    }
+    const size_t at = ((size_t)t * a.H + h) * a.chunks + ci;
+    if (live && ks == 0 && hf == 0) a.pml[at] = f32x2{__builtin_ldexpf(top, qexp - dk), l * unshift};
+    // the sums: each of those waves adds and writes a part of the registers, the others' through the stages
+    constexpr int QX = 4 / KS;  // quarters of a tile's registers that are this wave's
+    f32x4 *room = reinterpret_cast<f32x4 *>(&stage[0][0][0]);
+    auto place_of = [&](int from, int to) {  // [rw][from][to, but for from][quarter][tile][lane]
+        return room + ((((rw * KS + from) * (KS - 1) + (to > from ? to - 1 : to)) * QX) * MT) * kWave + lane;
+    };
+    static_assert(KS == 1 || sizeof(sh.stage) >= L::RW * KS * (KS - 1) * QX * MT * kWave * 16, "the waves' sums fit the stages");
+    f32x4 mine[QX][MT];
 #pragma unroll
-        for (int i = 0; i < MT; ++i) o[i] *= keep;
-        keep = 1.f;
-        if (ks > 0)
+    for (int x = 0; x < 4; ++x)
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    room[(((ks - 1) * L::RW + rw) * MT * 4 + 4 * i + x) * kWave + lane] =
-                        f32x4{o[i][4 * x], o[i][4 * x + 1], o[i][4 * x + 2], o[i][4 * x + 3]};
+        for (int i = 0; i < MT; ++i) {
+            const f32x4 v = f32x4{o[i][4 * x], o[i][4 * x + 1], o[i][4 * x + 2], o[i][4 * x + 3]} * keep;
+            if (KS == 1 || x / QX == ks)
+                mine[x % QX][i] = v;
+            else
+                place_of(ks, x / QX)[(x % QX * MT + i) * kWave] = v;
+        }
+    if constexpr (KS > 1) {
         __syncthreads();
-        if (ks > 0) return;
-        for (int y = 1; y < KS; ++y)
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
+        for (int y = 1; y < KS; ++y) {
+            const f32x4 *from = place_of((ks + y) % KS, ks);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const f32x4 v = room[(((y - 1) * L::RW + rw) * MT * 4 + 4 * i + x) * kWave + lane];
+            for (int x = 0; x < QX; ++x)
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) o[i][4 * x + z] += v[z];
-                }
+                for (int i = 0; i < MT; ++i) mine[x][i] += from[(x * MT + i) * kWave];
+        }
     }
     if (!live) return;
-    const size_t at = ((size_t)t * a.H + h) * a.chunks + ci;
-    if (hf == 0) a.pml[at] = f32x2{__builtin_ldexpf(top, qexp - dk), l * unshift};
-    float *dst = a.po + at * DH + 4 * hf;
+    const float back = __builtin_ldexpf(1.f, -dv);  // dv is between -113 and 133: not 0
+    float *dst = a.po + at * DH + 8 * QX * ks + 4 * hf;  // register 4 x + y of tile i: channel 32 i + 8 x + 4 hf + y
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int x = 0; x < QX; ++x)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            f32x4 v;
-#pragma unroll
-            for (int z = 0; z < 4; ++z) v[z] = __builtin_ldexpf(o[i][4 * x + z] * keep, -dv);
-            *(f32x4 *)(dst + 32 * i + 8 * x) = v;
-        }
+        for (int i = 0; i < MT; ++i) *(f32x4 *)(dst + 32 * i + 8 * x) = mine[x][i] * back;
 }
 
 // The shared positions' workgroups, then those of the sequences' own positions, which
