@@ -59,6 +59,8 @@ except ImportError:  # the library alone, on the system HIP runtime
     pass
 
 _lib = ctypes.CDLL(_LIB_PATH)
+if "torch" in globals():  # addresses of tensors, and the attention calls without ctypes' cost (csrc/marshal.cpp)
+    from . import _marshal
 _vp, _i, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
 
 
@@ -67,6 +69,11 @@ def _sig(name, restype, argtypes):
     f.restype = restype
     f.argtypes = argtypes
     return f
+
+
+def _call_sig(name, argtypes):
+    """An attention call: compiled where torch is, else as the others."""
+    return getattr(_marshal, name) if "_marshal" in globals() else _sig(name, _i, argtypes)
 
 
 _c_quantize = _sig("quantize_act_q8", _i, [_vp, _i, _i, _vp, _vp, _vp, _vp])
@@ -99,23 +106,23 @@ _c_moe_noalloc = _sig("moe_routed_qgemv_noalloc", _i, [_i, _vp, _vp, _vp, _i, _i
 _cache_sig = [_vp, _i, _i, _i, _vp]  # pages, max_pages, page, num_pages, kv
 _c_kv4_bytes = _sig("kv4_page_bytes", _sz, [_i, _i, _i])
 _kv4_sig = [_i, _vp, _i, _vp, _i, _i, _vp, _vp, _i, _i, _i, *_cache_sig, _vp, _vp]
-_c_kv4_append = _sig("kv4_append", _i, _kv4_sig)
-_c_kv4_gather = _sig("kv4_gather", _i, _kv4_sig)
+_c_kv4_append = _call_sig("kv4_append", _kv4_sig)
+_c_kv4_gather = _call_sig("kv4_gather", _kv4_sig)
 _c_decode_ws = _sig("attn_decode_workspace_bytes", _sz, [_i] * 7)
-_c_decode = _sig("attn_decode_kv4", _i, [_i, _vp, _i, _vp, _i, _i, _i, _i, _i, ctypes.c_float, _i, _i, *_cache_sig,
+_c_decode = _call_sig("attn_decode_kv4", [_i, _vp, _i, _vp, _i, _i, _i, _i, _i, ctypes.c_float, _i, _i, *_cache_sig,
                                          _vp, _vp, _sz, _vp, _vp])
-_c_attn_prefill = _sig("attn_prefill", _i, [_i, _vp, _i, _vp, _i, _vp, _i, _i, _i, _vp, _vp, _i, _i, _i, _i,
+_c_attn_prefill = _call_sig("attn_prefill", [_i, _vp, _i, _vp, _i, _vp, _i, _i, _i, _vp, _vp, _i, _i, _i, _i,
                                             ctypes.c_float, _i, _vp, _vp, _vp])
 
-_c_rope = _sig("qk_norm_rope", _i, [_i, _vp, _i, _vp, _i, _i, _vp, _vp, _i, _i, _i, _i, _vp, _vp, ctypes.c_float, _i, _i,
+_c_rope = _call_sig("qk_norm_rope", [_i, _vp, _i, _vp, _i, _i, _vp, _vp, _i, _i, _i, _i, _vp, _vp, ctypes.c_float, _i, _i,
                                     _vp, _i, _vp, _i, _vp, _i, _vp, _vp])
 _c_decode_sinks_ws = _sig("attn_decode_sinks_workspace_bytes", _sz, [_i] * 8)
-_c_decode_sinks = _sig("attn_decode_kv4_sinks", _i, [_i, _vp, _i, _vp, _i, _i, _i, _i, _i, ctypes.c_float, _i, _i, _i,
+_c_decode_sinks = _call_sig("attn_decode_kv4_sinks", [_i, _vp, _i, _vp, _i, _i, _i, _i, _i, ctypes.c_float, _i, _i, _i,
                                                      *_cache_sig, _vp, _vp, _sz, _vp, _vp])
-_c_prefill_sinks = _sig("attn_prefill_sinks", _i, [_i, _vp, _i, _vp, _i, _vp, _i, _i, _i, _vp, _vp, _i, _i, _i, _i,
+_c_prefill_sinks = _call_sig("attn_prefill_sinks", [_i, _vp, _i, _vp, _i, _vp, _i, _i, _i, _vp, _vp, _i, _i, _i, _i,
                                                    ctypes.c_float, _i, _i, _vp, _vp, _vp])
 _c_decode_prefix_ws = _sig("attn_decode_prefix_workspace_bytes", _sz, [_i] * 7)
-_c_decode_prefix = _sig("attn_decode_kv4_prefix", _i, [_i, _vp, _i, _vp, _i, _i, _i, _i, _i, ctypes.c_float, _i, _i, _vp,
+_c_decode_prefix = _call_sig("attn_decode_kv4_prefix", [_i, _vp, _i, _vp, _i, _i, _i, _i, _i, ctypes.c_float, _i, _i, _vp,
                                                        *_cache_sig, _vp, _vp, _sz, _vp, _vp])
 
 
@@ -285,10 +292,17 @@ if "torch" in globals():
                           lambda index: torch.cuda.current_stream(index).cuda_stream)
     _TYPES = {TYPE_F32: torch.float32, TYPE_F16: torch.float16, TYPE_BF16: torch.bfloat16}
     _I32, _FP32 = torch.int32, torch.float32
+    # the address of a tensor in which all is as it should be, or None
+    _plain_rows, _plain_array = _marshal.rows, _marshal.array
 else:
     class _Tensor:  # nothing is one
         pass
     _TYPES, _I32, _FP32 = {}, None, None
+
+    def _plain_rows(*_):
+        return None
+
+    _plain_array = _plain_rows
 
 
 def _device_of(first):
@@ -305,6 +319,9 @@ def _elsewhere(t, name: str, at: int, device):
 
 def _rows_ptr(t, name: str, device, type: int, rows: int, width: int, ld: int):
     """Device pointer of `rows` rows of `width` elements, `ld` elements apart."""
+    p = _plain_rows(t, device, type, rows, width, ld)
+    if p is not None:
+        return p
     if not isinstance(t, _Tensor):
         return _ptr(t)
     at = t.get_device()
@@ -330,6 +347,9 @@ def _rows_ptr(t, name: str, device, type: int, rows: int, width: int, ld: int):
 
 def _array_ptr(t, name: str, device, dtype, count: int):
     """Device pointer of a dense tensor that holds `count` values of dtype (None: any type, counted in bytes)."""
+    p = _plain_array(t, device, dtype, count)
+    if p is not None:
+        return p
     if not isinstance(t, _Tensor):
         return _ptr(t)
     at = t.get_device()
