@@ -25,7 +25,7 @@ struct RopeArgs {
     int32_t *status;
     int ldx[2], ldy[2];
     int n, B, H, heads, R;  // heads: of queries and keys
-    int waves, per;         // waves of a token, groups of heads of a wave
+    int waves;              // of a token
     float eps;
 };
 
@@ -70,11 +70,24 @@ __device__ __forceinline__ bool rope_lengths_ok(const RopeArgs &a, int c0, int c
     return c0 >= 0 && c1 >= c0 && c1 <= a.n && len >= c1 - c0 && len <= kRopeMaxLen;
 }
 
-template <int TIN, int TOUT, int DH, bool NEIGHBOURS, int PER>
+// Element j of 16 bytes.
+template <class T>
+__device__ __forceinline__ float element(u32x4 w, int j) {
+    if constexpr (sizeof(T) == 4) {
+        return __builtin_bit_cast(float, (uint32_t)w[j]);
+    } else {
+        typedef T pair __attribute__((ext_vector_type(2)));
+        return (float)__builtin_bit_cast(pair, (uint32_t)w[j / 2])[j % 2];
+    }
+}
+
+template <int TIN, int TOUT, int DH, bool NEIGHBOURS>
 __global__ __launch_bounds__(kRopeWaves *kWave) void qk_norm_rope_kernel(RopeArgs a) {
     typedef typename ElemOf<TIN>::type T;
     typedef typename ElemOf<TOUT>::type U;
-    constexpr int LANES = DH / 16, HEADS = kWave / LANES;  // lanes of a head, heads of a group
+    constexpr int LANES = DH / 16, HEADS = kWave / LANES;  // lanes of a head, heads of a wave
+    constexpr int E = 16 / (int)sizeof(T), NP = 16 / E;    // elements of 16 bytes, places of a lane
+    constexpr int NF = (DH / 2 + kWave - 1) / kWave;       // frequencies of a lane
     __shared__ __attribute__((aligned(16))) f32x2 turns[kRopeWaves][DH / 2];
     const int lane = lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int wave = blockIdx.x * kRopeWaves + wv;
@@ -84,94 +97,109 @@ __global__ __launch_bounds__(kRopeWaves *kWave) void qk_norm_rope_kernel(RopeArg
     const int tok = wave / a.waves;
     if (tok >= a.n) return;
 
-    // the lane's channels: pieces of 8 from at[0] and at[1] on, the pairs of frequencies 8 i..
-    const int i = lane % LANES;
-    const bool turned = 8 * i < a.R / 2;
-    const int at0 = NEIGHBOURS || !turned ? 16 * i : 8 * i, at1 = NEIGHBOURS || !turned ? 16 * i + 8 : a.R / 2 + 8 * i;
-    const int head0 = wave % a.waves * a.per * HEADS + lane / LANES;
-    Raw8<T> raw[PER][2];
+    // The lane's 16 channels: 16 bytes each of NP places, neighbouring lanes' side by side.
+    // Of the R / 16 lanes that turn, elements j and 8 + j are a pair of QG_ROPE_HALVES, 2 j and 2 j + 1 of
+    // QG_ROPE_NEIGHBOURS.
+    const int i = lane % LANES, turning = a.R / 16, h = wave % a.waves * HEADS + lane / LANES;
+    const bool turned = i < turning, mine = h < a.heads, key = h >= a.H;
+    int at[NP];
 #pragma unroll
-    for (int p = 0; p < PER; ++p) {
-        const int h = head0 + p * HEADS;
-        if (p < a.per && h < a.heads) {
-            const T *x = h < a.H ? (const T *)a.x[0] + (size_t)tok * a.ldx[0] + h * DH
-                                 : (const T *)a.x[1] + (size_t)tok * a.ldx[1] + (h - a.H) * DH;
-            raw[p][0] = load8(x + at0);
-            raw[p][1] = load8(x + at1);
-        }
+    for (int k = 0; k < NP; ++k) {
+        const int halves = k < NP / 2 ? E * (i + turning * k) : a.R / 2 + E * (i + turning * (k - NP / 2));
+        at[k] = !turned ? a.R + E * (i - turning + (LANES - turning) * k) : NEIGHBOURS ? E * (i + turning * k) : halves;
     }
-    const int b = wave_find_last(a.B, tok, [&](int s) { return a.cu[s]; });
-    const int c0 = load_uniform(a.cu + b), c1 = load_uniform(a.cu + b + 1), len = load_uniform(a.lens + b);
+    // all that is read, at once
+    u32x4 raw[NP];
+    f32x4 w[4];
+    float freq[NF];
+    const float *wp = a.w[key];
+    if (mine) {
+        const T *x = key ? (const T *)a.x[1] + (size_t)tok * a.ldx[1] + (h - a.H) * DH
+                         : (const T *)a.x[0] + (size_t)tok * a.ldx[0] + h * DH;
+#pragma unroll
+        for (int k = 0; k < NP; ++k) raw[k] = *(const u32x4 *)(x + at[k]);
+        if (wp)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = *(const f32x4 *)(wp + at[4 * j / E] + 4 * j % E);
+    }
+#pragma unroll
+    for (int f = 0; f < NF; ++f) freq[f] = f * kWave + lane < a.R / 2 ? a.freq[f * kWave + lane] : 0.f;
+    int c0, c1, len;
+    if (a.B <= kWave) {  // a sequence a lane: no second round trip
+        const int s = min(lane, a.B - 1), first = a.cu[s], end = a.cu[s + 1], held = a.lens[s];
+        const unsigned long long le = __ballot(lane < a.B && (lane == 0 || first <= tok));
+        const int b = 63 - __builtin_clzll(le);
+        c0 = __builtin_amdgcn_readlane(first, b);
+        c1 = __builtin_amdgcn_readlane(end, b);
+        len = __builtin_amdgcn_readlane(held, b);
+    } else {
+        const int b = wave_find_last(a.B, tok, [&](int s) { return a.cu[s]; });
+        c0 = load_uniform(a.cu + b);
+        c1 = load_uniform(a.cu + b + 1);
+        len = load_uniform(a.lens + b);
+    }
     if (!rope_lengths_ok(a, c0, c1, len) || tok < c0 || tok >= c1) return;
+
     const double pos = (double)(len - c1 + tok);
 #pragma unroll
-    for (int f = 0; f < (DH / 2 + kWave - 1) / kWave; ++f) {
-        const int at = f * kWave + lane;
-        if (at < a.R / 2) turns[wv][at] = cos_sin(pos * (double)a.freq[at]);
-    }
+    for (int f = 0; f < NF; ++f)
+        if (f * kWave + lane < DH / 2) turns[wv][f * kWave + lane] = cos_sin(pos * (double)freq[f]);
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
     f32x2 turn[8];
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-        const f32x4 t = turned ? *(const f32x4 *)&turns[wv][8 * i + j] : f32x4{1.f, 0.f, 1.f, 0.f};
+    for (int j = 0; j < 8; j += 2) {  // two frequencies side by side
+        const int f = NEIGHBOURS ? at[2 * j / E] / 2 + j % (E / 2) : at[j / E] + j % E;
+        const f32x4 t = turned ? *(const f32x4 *)&turns[wv][f] : f32x4{1.f, 0.f, 1.f, 0.f};
         turn[j] = f32x2{t[0], t[1]};
         turn[j + 1] = f32x2{t[2], t[3]};
     }
+    if (!mine) return;
+    float x[16];
 #pragma unroll
-    for (int p = 0; p < PER; ++p) {
-        const int h = head0 + p * HEADS;
-        if (p >= a.per || h - lane / LANES >= a.heads) break;
-        const bool key = h >= a.H;
-        float x[16];
+    for (int j = 0; j < 16; ++j) x[j] = element<T>(raw[j / E], j % E);
+    float sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = elem(raw[p][j / 8], j % 8);
-        float sum = 0.f;
+    for (int j = 0; j < 16; ++j) sum = __builtin_fmaf(x[j], x[j], sum);
+    sum = head_sum<LANES>(sum);
+    float eps = a.eps;
+    if (TIN != QG_TYPE_F16 && !(sum <= 0x1p126f)) {  // squares beyond fp32: all of it 2^64 times smaller
+        sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) sum = __builtin_fmaf(x[j], x[j], sum);
+        for (int j = 0; j < 16; ++j) {
+            x[j] *= 0x1p-64f;
+            sum = __builtin_fmaf(x[j], x[j], sum);
+        }
         sum = head_sum<LANES>(sum);
-        float eps = a.eps;
-        if (TIN != QG_TYPE_F16 && !(sum <= 0x1p126f)) {  // squares beyond fp32: all of it 2^64 times smaller
-            sum = 0.f;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                x[j] *= 0x1p-64f;
-                sum = __builtin_fmaf(x[j], x[j], sum);
-            }
-            sum = head_sum<LANES>(sum);
-            eps *= 0x1p-128f;
-        }
-        const float r = 1.f / __builtin_sqrtf(sum * (1.f / DH) + eps);
-        const float *w = a.w[key];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] *= r;
-        if (w)
-#pragma unroll
-            for (int j = 0; j < 16; ++j) x[j] *= w[(j < 8 ? at0 : at1) + j % 8];
-        float y[2][8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float &ya = NEIGHBOURS ? y[j / 4][2 * (j % 4)] : y[0][j], &yb = NEIGHBOURS ? y[j / 4][2 * (j % 4) + 1] : y[1][j];
-            const float xa = NEIGHBOURS ? x[2 * j] : x[j], xb = NEIGHBOURS ? x[2 * j + 1] : x[8 + j];
-            ya = __builtin_fmaf(xa, turn[j][0], -(xb * turn[j][1]));
-            yb = __builtin_fmaf(xb, turn[j][0], xa * turn[j][1]);
-        }
-        if (h < a.heads) {
-            U *o = key ? (U *)a.y[1] + (size_t)tok * a.ldy[1] + (h - a.H) * DH : (U *)a.y[0] + (size_t)tok * a.ldy[0] + h * DH;
-            store8(o + at0, y[0]);
-            store8(o + at1, y[1]);
-        }
+        eps *= 0x1p-128f;
     }
+    const float r = 1.f / __builtin_sqrtf(sum * (1.f / DH) + eps);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) x[j] *= r;
+    if (wp)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j] *= w[j / 4][j % 4];
+    U *y = key ? (U *)a.y[1] + (size_t)tok * a.ldy[1] + (h - a.H) * DH : (U *)a.y[0] + (size_t)tok * a.ldy[0] + h * DH;
+    typedef U out_t __attribute__((ext_vector_type(E)));
+    out_t out[NP];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int ja = NEIGHBOURS ? 2 * j : j, jb = NEIGHBOURS ? 2 * j + 1 : 8 + j;
+        out[ja / E][ja % E] = (U)__builtin_fmaf(x[ja], turn[j][0], -(x[jb] * turn[j][1]));
+        out[jb / E][jb % E] = (U)__builtin_fmaf(x[jb], turn[j][0], x[ja] * turn[j][1]);
+    }
+#pragma unroll
+    for (int k = 0; k < NP; ++k) *(out_t *)(y + at[k]) = out[k];
 }
 
 template <int TIN, int TOUT, int DH, bool NEIGHBOURS>
 static int launch_rope(RopeArgs a, hipStream_t stream) {
-    const int heads = kWave / (DH / 16), groups = (a.heads + heads - 1) / heads;
-    a.per = 1;
-    a.waves = groups;
+    constexpr int HEADS = 1024 / DH;
+    a.waves = (a.heads + HEADS - 1) / HEADS;
     const long long grid = ((long long)a.n * a.waves + kRopeWaves - 1) / kRopeWaves;
-    hipLaunchKernelGGL((qk_norm_rope_kernel<TIN, TOUT, DH, NEIGHBOURS, 1>), dim3((unsigned)grid), dim3(kRopeWaves * kWave), 0, stream, a);
+    hipLaunchKernelGGL((qk_norm_rope_kernel<TIN, TOUT, DH, NEIGHBOURS>), dim3((unsigned)grid), dim3(kRopeWaves * kWave), 0,
+                       stream, a);
     return hipGetLastError() == hipSuccess ? QG_OK : QG_ERR_LAUNCH;
 }
 
@@ -208,7 +236,7 @@ extern "C" int qk_norm_rope(int type, const void *q, int ldq, const void *k, int
         return QG_ERR_ALIGN;
     if (((uintptr_t)cu | (uintptr_t)lens | (uintptr_t)freq | (uintptr_t)d_status) & 3) return QG_ERR_ALIGN;
     RopeArgs a{{q, k}, {q_out, k_out}, {wq, wk}, freq, cu, lens, d_status, {ldq, ldk}, {ldq_out, ldk_out},
-               n, B, H, H + Hkv, R, 0, 0, eps};
+               n, B, H, H + Hkv, R, 0, eps};
     const bool neighbours = style == QG_ROPE_NEIGHBOURS;
     hipStream_t s = (hipStream_t)stream;
     clear_stale_error();
