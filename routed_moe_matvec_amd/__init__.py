@@ -292,17 +292,10 @@ if "torch" in globals():
                           lambda index: torch.cuda.current_stream(index).cuda_stream)
     _TYPES = {TYPE_F32: torch.float32, TYPE_F16: torch.float16, TYPE_BF16: torch.bfloat16}
     _I32, _FP32 = torch.int32, torch.float32
-    # the address of a tensor in which all is as it should be, or None
-    _plain_rows, _plain_array = _marshal.rows, _marshal.array
 else:
     class _Tensor:  # nothing is one
         pass
     _TYPES, _I32, _FP32 = {}, None, None
-
-    def _plain_rows(*_):
-        return None
-
-    _plain_array = _plain_rows
 
 
 def _device_of(first):
@@ -319,9 +312,6 @@ def _elsewhere(t, name: str, at: int, device):
 
 def _rows_ptr(t, name: str, device, type: int, rows: int, width: int, ld: int):
     """Device pointer of `rows` rows of `width` elements, `ld` elements apart."""
-    p = _plain_rows(t, device, type, rows, width, ld)
-    if p is not None:
-        return p
     if not isinstance(t, _Tensor):
         return _ptr(t)
     at = t.get_device()
@@ -347,9 +337,6 @@ def _rows_ptr(t, name: str, device, type: int, rows: int, width: int, ld: int):
 
 def _array_ptr(t, name: str, device, dtype, count: int):
     """Device pointer of a dense tensor that holds `count` values of dtype (None: any type, counted in bytes)."""
-    p = _plain_array(t, device, dtype, count)
-    if p is not None:
-        return p
     if not isinstance(t, _Tensor):
         return _ptr(t)
     at = t.get_device()
@@ -363,6 +350,12 @@ def _array_ptr(t, name: str, device, dtype, count: int):
     if have < count:
         raise ValueError("%s holds %d, the call needs %d" % (name, have, count))
     return t.data_ptr() if t.is_contiguous() else _ptr(t)
+
+
+if "_marshal" in globals():  # compiled for what is as it should be, and these for the rest
+    _checked_rows_ptr, _checked_array_ptr = _rows_ptr, _array_ptr
+    _marshal.otherwise(_checked_rows_ptr, _checked_array_ptr)
+    _rows_ptr, _array_ptr = _marshal.rows, _marshal.array
 
 
 def _call_on(what: str, f, first, index, args, stream):

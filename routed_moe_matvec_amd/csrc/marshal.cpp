@@ -3,7 +3,8 @@
 // from Python took 6 to 8 more, its arguments through ctypes 2.
 //
 //  rows, array   the address of a tensor that is on the call's device, of its type and
-//                large enough, or None: the binding then looks closer and says what is wrong
+//                large enough; for anything else what the binding's functions of the same
+//                arguments, which look closer and say what is wrong, return (otherwise(rows, array))
 //  the calls     of qgemv.h by their own names, addresses and sizes as integers; every
 //                call of the library runs without the interpreter's lock
 #include <Python.h>
@@ -37,15 +38,17 @@ bool numbers(PyObject *const *args, int n, long long *out) {
     return true;
 }
 
-// rows(tensor, device, type, rows, width, ld): rows of `width` elements, `ld` elements apart
-PyObject *rows(PyObject *, PyObject *const *args, Py_ssize_t n) {
+PyObject *other_rows, *other_array;
+
+// rows(tensor, name, device, type, rows, width, ld): rows of `width` elements, `ld` elements apart
+const void *find_rows(PyObject *const *args, Py_ssize_t n) {
     long long v[5];
-    if (n != 6 || !numbers(args + 1, 5, v)) Py_RETURN_NONE;
+    if (n != 7 || !numbers(args + 2, 5, v)) return nullptr;
     const long long type = v[1], count = v[2], width = v[3], ld = v[4];
     const at::Tensor *t = plain_tensor(args[0], v[0]);
-    if (!t || t->dim() == 0 || count < 1 || count > INT_MAX || ld > INT_MAX) Py_RETURN_NONE;
+    if (!t || t->dim() == 0 || count < 1 || count > INT_MAX || ld > INT_MAX) return nullptr;
     const at::ScalarType want = type == QG_TYPE_F32 ? at::kFloat : type == QG_TYPE_F16 ? at::kHalf : at::kBFloat16;
-    if (type > QG_TYPE_BF16 || t->scalar_type() != want) Py_RETURN_NONE;
+    if (type > QG_TYPE_BF16 || t->scalar_type() != want) return nullptr;
     const auto shape = t->sizes(), steps = t->strides();
     const long long have = t->numel();
     bool fits;
@@ -60,23 +63,36 @@ PyObject *rows(PyObject *, PyObject *const *args, Py_ssize_t n) {
         }
         fits = fits && each == width;
     }
-    if (!fits) Py_RETURN_NONE;
-    return PyLong_FromVoidPtr(t->data_ptr());
+    return fits ? t->data_ptr() : nullptr;
 }
 
-// array(tensor, device, dtype, count): a dense tensor of `count` values of dtype, or of bytes (None)
-PyObject *array(PyObject *, PyObject *const *args, Py_ssize_t n) {
+// array(tensor, name, device, dtype, count): a dense tensor of `count` values of dtype, or of bytes (None)
+const void *find_array(PyObject *const *args, Py_ssize_t n) {
     long long device, count;
-    if (n != 4 || !numbers(args + 1, 1, &device) || !numbers(args + 3, 1, &count)) Py_RETURN_NONE;
+    if (n != 5 || !numbers(args + 2, 1, &device) || !numbers(args + 4, 1, &count)) return nullptr;
     const at::Tensor *t = plain_tensor(args[0], device);
-    if (!t || !t->is_contiguous()) Py_RETURN_NONE;
+    if (!t || !t->is_contiguous()) return nullptr;
     long long have = t->numel();
-    if (args[2] == Py_None)
+    if (args[3] == Py_None)
         have *= t->element_size();
-    else if (!THPDtype_Check(args[2]) || t->scalar_type() != reinterpret_cast<THPDtype *>(args[2])->scalar_type)
-        Py_RETURN_NONE;
-    if (have < count) Py_RETURN_NONE;
-    return PyLong_FromVoidPtr(t->data_ptr());
+    else if (!THPDtype_Check(args[3]) || t->scalar_type() != reinterpret_cast<THPDtype *>(args[3])->scalar_type)
+        return nullptr;
+    return have < count ? nullptr : t->data_ptr();
+}
+
+template <auto FIND, PyObject **OTHER>
+PyObject *address(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    if (const void *p = FIND(args, n)) return PyLong_FromVoidPtr(const_cast<void *>(p));
+    return PyObject_Vectorcall(*OTHER, args, n, nullptr);
+}
+
+PyObject *otherwise(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    if (n != 2) return PyErr_Format(PyExc_TypeError, "two functions are needed");
+    Py_INCREF(args[0]);
+    Py_INCREF(args[1]);
+    Py_XSETREF(other_rows, args[0]);
+    Py_XSETREF(other_array, args[1]);
+    Py_RETURN_NONE;
 }
 
 template <class A>
@@ -119,8 +135,9 @@ PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t n) {
 }
 
 #define METHOD(name, f) {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {METHOD("rows", rows),
-                         METHOD("array", array),
+PyMethodDef methods[] = {METHOD("rows", (address<find_rows, &other_rows>)),
+                         METHOD("array", (address<find_array, &other_array>)),
+                         METHOD("otherwise", otherwise),
                          METHOD("kv4_append", call<kv4_append>),
                          METHOD("kv4_gather", call<kv4_gather>),
                          METHOD("attn_decode_kv4", call<attn_decode_kv4>),
@@ -134,4 +151,8 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__marshal() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__marshal() {
+    other_rows = Py_NewRef(Py_None);
+    other_array = Py_NewRef(Py_None);
+    return PyModule_Create(&module);
+}
