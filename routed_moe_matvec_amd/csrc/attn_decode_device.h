@@ -571,6 +571,7 @@ __device__ __forceinline__ void attn_decode_group(const DecodeArgs &a, DecShared
     const int wk = threadIdx.x & 3, wc = (threadIdx.x >> 2) % ROWS, wg = threadIdx.x >> 6;
     const int wi = (threadIdx.x >> 2) % 16 / ROWS * PART;
     const bool adds = WAVES == 4 || threadIdx.x < 256;
+    const int busy = (last - first + kDecStep - 1) / kDecStep;  // waves that had positions, or more
     const int wrow = row0 + wc;
     const int wt = token_of(wrow);
     const size_t wout = (size_t)(b * a.Tq + wt) * a.H + hk * a.G + wrow - wt * a.G;
@@ -587,21 +588,27 @@ __device__ __forceinline__ void attn_decode_group(const DecodeArgs &a, DecShared
     for (int y = 0; y < DecTile<DH>::VC; ++y) {
         if (y) __syncthreads();
 #pragma unroll
-        for (int i = 0; i < PER; ++i) so[(wave * PER + i) * kWave + lane] = o[8 * y + i] * keep;
+        for (int i = 0; i < PER; ++i)
+            if (WAVES == 4 || wave < 4 || busy > 4) so[(wave * PER + i) * kWave + lane] = o[8 * y + i] * keep;
         __syncthreads();
         if (!adds) continue;
         float acc[PART];
 #pragma unroll
-        for (int i = 0; i < PART; ++i) {
-            acc[i] = 0.f;
+        for (int i = 0; i < PART; ++i) acc[i] = 0.f;
+        auto add_waves = [&](int from, int to) {
 #pragma unroll
-            for (int w = 0; w < WAVES; ++w)
+            for (int i = 0; i < PART; ++i)
 #pragma unroll
-                for (int x = 0; x < SLOTS; ++x)
-                    acc[i] += reinterpret_cast<const float *>(
-                        &so[(w * PER + wi + i) * kWave + 16 * wg + wc + x * ROWS])[wk];
-            acc[i] *= f;
-        }
+                for (int w = from; w < to; ++w)
+#pragma unroll
+                    for (int x = 0; x < SLOTS; ++x)
+                        acc[i] += reinterpret_cast<const float *>(
+                            &so[(w * PER + wi + i) * kWave + 16 * wg + wc + x * ROWS])[wk];
+        };
+        add_waves(0, 4);
+        if (WAVES > 4 && busy > 4) add_waves(4, WAVES);
+#pragma unroll
+        for (int i = 0; i < PART; ++i) acc[i] *= f;
         if (wrow < R) {
             float *at = dst + (16 * y + 4 * wg + wk) * PER + wi;
             if constexpr (PART >= 4) {
