@@ -101,6 +101,19 @@ __device__ __forceinline__ int wave_sum(int x) {
     return __builtin_amdgcn_readlane(x, 63);
 }
 
+// Maximum over the wave, the same in every lane.
+__device__ __forceinline__ int wave_max(int x) {
+#define QG_DPP_MAX(ctrl, rows) x = max(x, __builtin_amdgcn_update_dpp(x, x, ctrl, rows, 0xf, false))
+    QG_DPP_MAX(0x111, 0xf);  // as above
+    QG_DPP_MAX(0x112, 0xf);
+    QG_DPP_MAX(0x114, 0xf);
+    QG_DPP_MAX(0x118, 0xf);
+    QG_DPP_MAX(0x142, 0xa);
+    QG_DPP_MAX(0x143, 0xc);
+#undef QG_DPP_MAX
+    return __builtin_amdgcn_readlane(x, 63);
+}
+
 // One workgroup's queries: sequence b's tile t, or nothing.
 struct PreWork {
     bool any;
@@ -124,21 +137,9 @@ __device__ __forceinline__ PreWork pre_by_rank(const PrefillArgs &a, int rank) {
     PreWork w{false, 0, 0, 0, 0, 0};
     if (rank >= wave_sum(tiles)) return w;
     auto at_least = [&](int x) { return wave_sum(min(max(tiles + min(base - x, 0), 0), tiles)); };
-    int lo = 0, hi = 2 * (QG_MAX_ATTN_TOKENS / ROWS) + 2;  // at_least(lo) > rank >= at_least(hi)
-    // mostly among the first sequence's buckets
-    const int own = __builtin_amdgcn_readfirstlane(base), top = own + __builtin_amdgcn_readfirstlane(tiles);
-    if (own > 0) {
-        if (at_least(own) > rank)
-            lo = own;
-        else
-            hi = own;
-        if (top > lo && top < hi) {
-            if (at_least(top) > rank)
-                lo = top;
-            else
-                hi = top;
-        }
-    }
+    // at_least(lo) > rank >= at_least(hi): between the least and the most keys that a tile sees (searching
+    // all that there may be took 1 us of a workgroup's 2 here)
+    int lo = -wave_max(tiles ? -base : -(1 << 30)), hi = wave_max(tiles ? base + tiles : 0);
     while (hi - lo > 1) {
         const int mid = lo + (hi - lo) / 2;
         if (at_least(mid) > rank)
@@ -309,20 +310,17 @@ __global__ __launch_bounds__(kPreWaves *kWave, DH == 256 || KS == 4 ? 1 : DH == 
         const int j0 = next + r0 + (SINKS && next < edge ? 0 : gap);
         if constexpr (do_s.value) {
             // register 4 x + y of tile n: key 32 n + 8 x + 4 hf + y
-            if (SINKS && next < edge) {
-                if (j0 + OWN > a.sinks)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (j0 + 32 * n + 8 * (j / 4) + 4 * hf + j % 4 >= a.sinks) t[n][j] = -INFINITY;
-            } else if (j0 + OWN > wi0 + shift + 1 || (a.window && j0 < w_hi - a.window)) {
+            const bool of_sinks = SINKS && next < edge;  // a tile of them sees no more than them
+            const int lo = of_sinks ? see_hi : see_lo;
+            if (of_sinks ? j0 + OWN > a.sinks : j0 + OWN > wi0 + shift + 1 || (a.window && j0 < w_hi - a.window)) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         const int key = j0 + 32 * n + 8 * (j / 4) + 4 * hf + j % 4;
-                        if (key >= see_hi || (key < see_lo && (!SINKS || key >= a.sinks))) t[n][j] = -INFINITY;
+                        // no short circuits: they become branches, one an element
+                        if (SINKS ? (key >= see_hi) | ((key < lo) & (key >= a.sinks)) : key >= see_hi || key < lo)
+                            t[n][j] = -INFINITY;
                     }
             }
         }
