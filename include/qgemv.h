@@ -668,10 +668,12 @@ int attn_prefill_sinks(int type, const void *q, int ldq, const void *k, int ldk,
  * the prefix; a sequence may also end inside it (lens[b] = 0 for an unused row of the batch).
  * prefix = 0 (prefix_pages may be NULL) is attn_decode_kv4.  Results agree with
  * attn_decode_kv4's over a table whose blocks name the same keys and values to rounding; one
- * sequence's may depend on the batch by rounding.
+ * sequence's may depend on the batch by rounding.  The error is as there, but that
+ * weights over the prefix below 2^-11 of a row's largest may be off by 2^-36 of it.
  * ws: attn_decode_prefix_workspace_bytes(...) bytes.
  * Data errors: as attn_decode_kv4; a bad page of the prefix is left out for all.
- * Errors: as attn_decode_kv4; QG_ERR_SHAPE unless 0 <= prefix <= max_len.
+ * Errors: as attn_decode_kv4; QG_ERR_SHAPE unless 0 <= prefix <= max_len, and where its
+ * launch would need 2^24 workgroups.
  */
 size_t attn_decode_prefix_workspace_bytes(int B, int Tq, int H, int Hkv, int Dh, int max_len, int prefix);
 int attn_decode_kv4_prefix(int type, const void *q, int ldq, const int32_t *lens, int B, int Tq, int H, int Hkv,

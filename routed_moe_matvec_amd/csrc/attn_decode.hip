@@ -231,7 +231,8 @@ static int decode(int type, const void *q, int ldq, const int32_t *lens, int B, 
     a.split = n.own;
     a.po = (float *)ws;
     a.pml = (f32x2 *)((uint8_t *)ws + (a.chunks == 1 && !a.prefix_chunks ? 0 : decode_sums_bytes(B, Tq, H, Dh, a.chunks)));
-    if ((long long)Hkv * B * a.chunks * ((a.G * Tq + 15) / 16) > kMaxGroups || (long long)H * Tq * B > kMaxGroups)
+    if ((!n.prefix.chunks && (long long)Hkv * B * a.chunks * ((a.G * Tq + 15) / 16) > kMaxGroups) ||
+        (long long)H * Tq * B > kMaxGroups)
         return QG_ERR_SHAPE;
     clear_stale_error();
     switch (type) {

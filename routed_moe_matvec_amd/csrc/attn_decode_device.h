@@ -279,6 +279,10 @@ __device__ __forceinline__ void attn_decode_group(const DecodeArgs &a, DecShared
     const int b = bi % a.c.B, ci = bi / a.c.B;
     const int row0 = tile * ROWS;
     const int R = a.G * a.Tq;
+    if (MODE == TAIL && ci > 0) {  // before anything is asked for: max_len may be far above the lengths
+        const int n = dec_range<TAIL>(a, b).n;
+        if (n <= 0 || ci >= a.split.chunks(n)) return;
+    }
     const int c = lane & 15, g = lane >> 4;
     const int row = row0 + c % ROWS;
     const uint32_t second = c / ROWS ? ~0u : 0u;  // columns of the second, or no, part
