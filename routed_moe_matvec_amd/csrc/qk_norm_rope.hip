@@ -100,8 +100,10 @@ __global__ __launch_bounds__(kRopeWaves *kWave) void qk_norm_rope_kernel(RopeArg
     // The lane's 16 channels: 16 bytes each of NP places, neighbouring lanes' side by side.
     // Of the R / 16 lanes that turn, elements j and 8 + j are a pair of QG_ROPE_HALVES, 2 j and 2 j + 1 of
     // QG_ROPE_NEIGHBOURS.
-    const int i = lane % LANES, turning = a.R / 16, h = wave % a.waves * HEADS + lane / LANES;
-    const bool turned = i < turning, mine = h < a.heads, key = h >= a.H;
+    const int i = lane % LANES, turning = a.R / 16, asked = wave % a.waves * HEADS + lane / LANES;
+    const bool turned = i < turning, mine = asked < a.heads;
+    const int h = mine ? asked : 0;  // lanes behind the last head read the first, and write nothing
+    const bool key = h >= a.H;
     int at[NP];
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
@@ -112,16 +114,16 @@ __global__ __launch_bounds__(kRopeWaves *kWave) void qk_norm_rope_kernel(RopeArg
     u32x4 raw[NP];
     f32x4 w[4];
     float freq[NF];
+    const T *xp = key ? (const T *)a.x[1] + (size_t)tok * a.ldx[1] + (h - a.H) * DH
+                      : (const T *)a.x[0] + (size_t)tok * a.ldx[0] + h * DH;
     const float *wp = a.w[key];
-    if (mine) {
-        const T *x = key ? (const T *)a.x[1] + (size_t)tok * a.ldx[1] + (h - a.H) * DH
-                         : (const T *)a.x[0] + (size_t)tok * a.ldx[0] + h * DH;
 #pragma unroll
-        for (int k = 0; k < NP; ++k) raw[k] = *(const u32x4 *)(x + at[k]);
-        if (wp)
+    for (int k = 0; k < NP; ++k) raw[k] = *(const u32x4 *)(xp + at[k]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = *(const f32x4 *)(wp + at[4 * j / E] + 4 * j % E);
-    }
+    for (int j = 0; j < 4; ++j) w[j] = f32x4{1.f, 1.f, 1.f, 1.f};
+    if (wp)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = *(const f32x4 *)(wp + at[4 * j / E] + 4 * j % E);
 #pragma unroll
     for (int f = 0; f < NF; ++f) freq[f] = f * kWave + lane < a.R / 2 ? a.freq[f * kWave + lane] : 0.f;
     int c0, c1, len;
@@ -149,9 +151,9 @@ __global__ __launch_bounds__(kRopeWaves *kWave) void qk_norm_rope_kernel(RopeArg
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
     f32x2 turn[8];
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {  // two frequencies side by side
-        const int f = NEIGHBOURS ? at[2 * j / E] / 2 + j % (E / 2) : at[j / E] + j % E;
-        const f32x4 t = turned ? *(const f32x4 *)&turns[wv][f] : f32x4{1.f, 0.f, 1.f, 0.f};
+    for (int j = 0; j < 8; j += 2) {  // two frequencies side by side; those from R / 2 on are 0: no turn
+        const int own = NEIGHBOURS ? at[2 * j / E] / 2 + j % (E / 2) : at[j / E] + j % E, f = turned ? own : a.R / 2 + j;
+        const f32x4 t = *(const f32x4 *)&turns[wv][f];
         turn[j] = f32x2{t[0], t[1]};
         turn[j + 1] = f32x2{t[2], t[3]};
     }
@@ -177,9 +179,8 @@ __global__ __launch_bounds__(kRopeWaves *kWave) void qk_norm_rope_kernel(RopeArg
     const float r = 1.f / __builtin_sqrtf(sum * (1.f / DH) + eps);
 #pragma unroll
     for (int j = 0; j < 16; ++j) x[j] *= r;
-    if (wp)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] *= w[j / 4][j % 4];
+    for (int j = 0; j < 16; ++j) x[j] *= w[j / 4][j % 4];
     U *y = key ? (U *)a.y[1] + (size_t)tok * a.ldy[1] + (h - a.H) * DH : (U *)a.y[0] + (size_t)tok * a.ldy[0] + h * DH;
     typedef U out_t __attribute__((ext_vector_type(E)));
     out_t out[NP];
