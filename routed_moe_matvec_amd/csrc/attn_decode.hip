@@ -18,6 +18,13 @@
 // Products and sums are fp32.  The running maximum is one of q . k, not
 // scaled, and is taken off the scores themselves where it is large (RunningMax; 0
 // to 3% of the time).
+//
+// The same walk serves windows with first positions that stay visible (SINKS) and short
+// shared prefixes (FUSED): places are counted over two ranges of positions, each from a
+// multiple of 16, and a tile lies in one of them.  32 sequences of up to 20000 positions with a window
+// of 1024 and 4 sinks, 32 heads of 128: 10.9 us, 35 MB; 24 of up to 60000 with a window of
+// 8192 and 100 sinks, 3 tokens, 16 heads of 64: 58 us, 196 MB, bound by vector
+// instructions (76% of the cycles: every cached value is converted for 3 rows only).
 #include <type_traits>
 
 #include "attn_decode_device.h"
