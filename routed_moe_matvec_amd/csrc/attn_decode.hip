@@ -24,7 +24,8 @@
 // multiple of 16, and a tile lies in one of them.  32 sequences of up to 20000 positions with a window
 // of 1024 and 4 sinks, 32 heads of 128: 10.9 us, 35 MB; 24 of up to 60000 with a window of
 // 8192 and 100 sinks, 3 tokens, 16 heads of 64: 58 us, 196 MB, bound by vector
-// instructions (76% of the cycles: every cached value is converted for 3 rows only).
+// instructions (76% of the cycles, without the issue of matrix instructions: every cached value
+// is converted for 3 rows only).
 #include <type_traits>
 
 #include "attn_decode_device.h"

@@ -184,8 +184,9 @@ __device__ __forceinline__ PreWork pre_by_slot(const PrefillArgs &a, int slot) {
 // the sinks (the last tile filled up with the last of them, masked), what follows is
 // `gap` further on (or less: the sinks' last tile may reach into it).  16384 tokens of 32
 // heads of 128, window 4096 and 64 sinks: 1000 us, 970 TFLOP/s of visible pairs; six prompts of 1
-// to 3301, window 512 and 4 sinks: 83 us, 490: a window's first and last tiles are a third of its
-// eleven.  Two waves of a workgroup sharing 64 queries there: 103 -> 110 (64 channels 64 -> 58, 256 250 -> 280).
+// to 3301, window 512 and 4 sinks: 83 us, 490: 69% of the pairs of their tiles (128 queries, 64
+// keys) are visible, and half of the tiles need a mask.  64 queries a workgroup there, two waves sharing
+// each 32, in a graph: 103 -> 110 (64 channels 64 -> 58, 256 250 -> 280).
 template <int TYPE, int DH, int KS, bool SINKS>
 __global__ __launch_bounds__(kPreWaves *kWave, DH == 256 || KS == 4 ? 1 : DH == 64 && KS == 2 ? 4 : 2) void attn_prefill_kernel(PrefillArgs a) {
     typedef typename ElemOf<TYPE>::type T;

@@ -15,13 +15,12 @@
 // within 2^26 of the row's largest, else the chunk is not taken so) and an fp16 one itself.  Other
 // chunks, and the keys of bf16 queries, take bf16, which holds every value exactly, and
 // three parts for 24 bits: fp32, fp16, bf16 queries need 4, 3, 3 products so, and 6, 5, 4 there
-// (whose queries are read and split again at every tile).  Each product counts: 48 sequences of 8
-// rows a head over 40001 positions take 126 us, of which 4 / 2 of the 63 GFLOP's time at the
-// 1.1 PFLOP/s that long prompts reach here are 115; the matrix cores are busy 52% of the cycles, the
-// vector units 47%, both at once 19%, and neither another order of the instructions nor wave
-// priorities changed that (2.1 GHz: power).  The same rows with operands made for 64 rows by each wave from
-// its own positions, queries in LDS, took 167: a product waited for each read.  Few positions are bound
-// by latency: 4.3 us to the first tile, 2.8 for it, 1.7 for each further one of 128, 2 for the sums.
+// (fp32 and fp16 queries are read and split again at every tile).  48 sequences of 8 rows a head of
+// fp32 queries over 40001 positions, 63 GFLOP, 127 with the parts, take 125 to 146 us by the run: the
+// matrix cores are busy 52% of the cycles, the vector units 47% (without the issue of matrix
+// instructions), both at once 19%, at 2.1 GHz, and neither another order of the instructions nor wave
+// priorities changed that.  Few positions are bound by latency.  32 sequences of 4 rows over 6001: 4.3
+// us to the first tile, 2.8 for it, 1.7 for each further one of 128, 2 for the sums.
 #include <type_traits>
 
 #include "attn_decode_device.h"

@@ -10,12 +10,11 @@
 // sums of their power series there, in fp32.  A wave computes those of its token
 // once, a lane each, and shares them through LDS.
 //
-// Bound by memory: 31 k tokens of 40 heads of 128 in bf16 114 us, 5.6 TB/s (a copy of the
-// size reaches 5.1 to 5.5), 4094 tokens of 20 heads of 256 from fp32 to bf16 20.8 us,
-// 6.0 TB/s.  A wave with two to five groups of heads, its sines shared by them: the same
-// to 8% slower, and a step's latency 3.3 -> 3.9 to 5.7 us.  Small calls are one round
-// trip to memory: everything is asked for at once, the token's sequence found among
-// up to 64 by one ballot (32 tokens: 3.6 -> 3.1 us).
+// Bound by memory: 31 k tokens of 40 heads of 128 in bf16 112 to 118 us, 5.4 to 5.7 TB/s (copies
+// of such sizes reach 5.1 to 5.5), 4094 tokens of 20 heads of 256 from fp32 to bf16 21 us,
+// 6.0 TB/s, part of it in the last-level cache.  A wave with two to five groups of heads, its
+// sines shared by them, took 3% less to 8% more for these two, and 3.8 to 5.5 us for 32 tokens in
+// place of 3.4.  Small calls are one round trip to memory, so everything is asked for at once.
 #include <type_traits>
 
 #include "common.h"
