@@ -10,7 +10,7 @@
 // sums of their power series there, in fp32.  A wave computes those of its token
 // once, a lane each, and shares them through LDS.
 //
-// Bound by memory: 31 k tokens of 40 heads of 128 in bf16 112 to 118 us, 5.4 to 5.7 TB/s (copies
+// Bound by memory: 31 k tokens of 40 heads of 128 in bf16 112 to 124 us, 5.1 to 5.7 TB/s (copies
 // of such sizes reach 5.1 to 5.5), 4094 tokens of 20 heads of 256 from fp32 to bf16 21 us,
 // 6.0 TB/s, part of it in the last-level cache.  A wave with two to five groups of heads, its
 // sines shared by them, took 3% less to 8% more for these two, and 3.8 to 5.5 us for 32 tokens in
@@ -157,8 +157,8 @@ __global__ __launch_bounds__(kRopeWaves *kWave) void qk_norm_rope_kernel(RopeArg
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
     f32x2 turn[8];
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {  // two frequencies side by side; those from R / 2 on are 0: no turn
-        const int own = NEIGHBOURS ? at[2 * j / E] / 2 + j % (E / 2) : at[j / E] + j % E, f = turned ? own : a.R / 2 + j;
+    for (int j = 0; j < 8; j += 2) {  // two frequencies side by side
+        const int own = NEIGHBOURS ? at[2 * j / E] / 2 + j % (E / 2) : at[j / E] + j % E, f = turned ? own : 0;
         const f32x4 t = *(const f32x4 *)&turns[wv][f];
         turn[j] = f32x2{t[0], t[1]};
         turn[j + 1] = f32x2{t[2], t[3]};
@@ -193,8 +193,11 @@ __global__ __launch_bounds__(kRopeWaves *kWave) void qk_norm_rope_kernel(RopeArg
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const int ja = NEIGHBOURS ? 2 * j : j, jb = NEIGHBOURS ? 2 * j + 1 : 8 + j;
-        out[ja / E][ja % E] = (U)__builtin_fmaf(x[ja], turn[j][0], -(x[jb] * turn[j][1]));
-        out[jb / E][jb % E] = (U)__builtin_fmaf(x[jb], turn[j][0], x[ja] * turn[j][1]);
+        // what does not turn is not multiplied with its neighbour's 0 either: that may be Inf or NaN
+        const float ya = __builtin_fmaf(x[ja], turn[j][0], -(x[jb] * turn[j][1]));
+        const float yb = __builtin_fmaf(x[jb], turn[j][0], x[ja] * turn[j][1]);
+        out[ja / E][ja % E] = (U)(turned ? ya : x[ja]);
+        out[jb / E][jb % E] = (U)(turned ? yb : x[jb]);
     }
 #pragma unroll
     for (int k = 0; k < NP; ++k) *(out_t *)(y + at[k]) = out[k];

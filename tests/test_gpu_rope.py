@@ -169,6 +169,30 @@ def test_infinities_and_nan_stay_in_their_head(qg):
     assert torch.equal(got[rest], want[rest])
 
 
+@pytest.mark.parametrize("neighbours", [False, True])
+@pytest.mark.parametrize("type", [0, 1, 2])
+def test_channels_that_do_not_turn_are_by_themselves(qg, type, neighbours):
+    """y_c = u_c there: an infinity makes its own channel NaN (Inf * 0) and the others of its head 0, and a weight that is
+    none its own channel only."""
+    progress("rope apart type %d" % type)
+    for Dh, R in ((64, 16), (128, 0), (128, 96), (256, 64)):
+        for c in (R, R + 1, Dh - 9, Dh - 1):
+            x = sh.normal(6, (2, 3, Dh), TYPES[type])
+            x[1, 1, c] = math.inf
+            got, _, _ = call(qg, x, x[:, :1], [2], [2], R, neighbours, type)
+            want = torch.zeros(Dh, device="cuda")
+            want[c] = math.nan
+            assert torch.equal(got[1, 1].float().nan_to_num(9.0), want.nan_to_num(9.0)), (Dh, R, c)
+            x = sh.normal(6, (2, 3, Dh), TYPES[type])
+            w = torch.ones(Dh, device="cuda")
+            plain, _, _ = call(qg, x, x[:, :1], [2], [2], R, neighbours, type, wq=w)
+            w[c] = math.nan
+            got, _, _ = call(qg, x, x[:, :1], [2], [2], R, neighbours, type, wq=w)
+            assert bool(got[..., c].isnan().all())
+            plain[..., c] = got[..., c] = 0
+            assert torch.equal(got, plain), (Dh, R, c)
+
+
 def test_data_errors(qg):
     """The faulty sequence is left out and reported, the others are computed."""
     progress("rope data errors")
