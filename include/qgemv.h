@@ -627,7 +627,8 @@ int attn_prefill(int type, const void *q, int ldq, const void *k, int ldk, const
  * sequence may be left out too.
  * Errors: QG_ERR_FORMAT (types, style); QG_ERR_NULL; QG_ERR_SHAPE unless 1 <= n <=
  * QG_MAX_ATTN_TOKENS, 1 <= B <= QG_MAX_SEQS, 1 <= H, Hkv <= QG_MAX_HEADS, Dh as above,
- * 0 <= R <= Dh, R % 16 == 0, 2^-100 <= eps <= 2^100, row strides as above, or if
+ * 0 <= R <= Dh, R % 16 == 0, 2^-100 <= eps <= 2^100, row strides as above, if q_out is q
+ * or k_out is k with another type or row stride, or if
  * n * ceil((H + Hkv) * Dh / 1024) >= 2^26 - 3 (one launch); QG_ERR_ALIGN; QG_ERR_LAUNCH.
  */
 int qk_norm_rope(int type, const void *q, int ldq, const void *k, int ldk, int n, const int32_t *cu,

@@ -245,6 +245,9 @@ extern "C" int qk_norm_rope(int type, const void *q, int ldq, const void *k, int
     if (((uintptr_t)q | (uintptr_t)k | (uintptr_t)q_out | (uintptr_t)k_out | (uintptr_t)wq | (uintptr_t)wk) & 15)
         return QG_ERR_ALIGN;
     if (((uintptr_t)cu | (uintptr_t)lens | (uintptr_t)freq | (uintptr_t)d_status) & 3) return QG_ERR_ALIGN;
+    // in place, but rows of another type or stride would land on heads that other waves still read
+    if ((q_out == q && (out_type != type || ldq_out != ldq)) || (k_out == k && (out_type != type || ldk_out != ldk)))
+        return QG_ERR_SHAPE;
     RopeArgs a{{q, k}, {q_out, k_out}, {wq, wk}, freq, cu, lens, d_status, {ldq, ldk}, {ldq_out, ldk_out},
                n, B, H, H + Hkv, R, 0, eps};
     const bool neighbours = style == QG_ROPE_NEIGHBOURS;

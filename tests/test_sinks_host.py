@@ -59,6 +59,14 @@ def test_rope_refuses(lib):
         assert _call(lib, "qk_norm_rope", ROPE_T, {**ROPE, **rows, "n": 1 << 24, "cu": AT + 1}) == code
 
 
+def test_rope_in_place_refuses_other_types_and_strides(lib):
+    """A row of another type or stride would be written over heads that other waves still read."""
+    apart = dict(q_out=AT + (1 << 20), k_out=AT + (1 << 21))
+    for change in (dict(q_out=AT), dict(k_out=AT), dict(out_type=0, q_out=AT, ldq_out=1024),
+                   dict(out_type=0, k_out=AT, ldk_out=512)):
+        assert _call(lib, "qk_norm_rope", ROPE_T, {**ROPE, **apart, **change}) == -2, change
+
+
 @pytest.mark.parametrize("change,code", BAD_DECODE + [(dict(sinks=-1), -2)])
 def test_sinks_decode_refuses(lib, change, code):
     assert _call(lib, "attn_decode_kv4_sinks", SINKS_T, {**SINKS, **change}) == code
