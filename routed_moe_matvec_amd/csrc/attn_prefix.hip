@@ -100,7 +100,7 @@ struct PfxShared {
     char stage[PfxTile<DH, KS>::STAGES][2][PfxTile<DH, KS>::BYTES];
     f32x2 ml[KS][kDecWaves][32];
     u16x2 bytes[2][kDecWaves];  // of the chunk's key and value scales: the largest, and 255 less the least
-    int bad[kDecWaves], wide[kDecWaves];
+    int bad[kDecWaves], wide[kDecWaves], seen[kDecWaves];
     int page[kDecChunkMax / 16];
 };
 
@@ -133,12 +133,12 @@ __device__ __forceinline__ void attn_prefix_group(const DecodeArgs &a, PfxShared
         }
     }
     const int hk = u % a.c.Hkv, ci = u / a.c.Hkv;
-    const int first = ci * a.prefix_each, last = min(a.prefix, first + a.prefix_each);
+    const int first = ci * a.prefix_each, end = min(a.prefix, first + a.prefix_each);
     const int page = 1 << a.c.page_log2, pg0 = first >> a.c.page_log2;
     const size_t region = kv4_region_bytes(page, DH);
 
     bool bad = false;
-    for (int i = tid; i <= ((last - 1) >> a.c.page_log2) - pg0; i += kDecWaves * kWave) {
+    for (int i = tid; i <= ((end - 1) >> a.c.page_log2) - pg0; i += kDecWaves * kWave) {
         spage[i] = kv4_page_of(prefix, 0, pg0 + i);
         bad |= spage[i] < 0;
     }
@@ -152,17 +152,29 @@ __device__ __forceinline__ void attn_prefix_group(const DecodeArgs &a, PfxShared
     Raw8<T> qraw[KC];
 #pragma unroll
     for (int i = 0; i < KC; ++i) qraw[i] = load8(qp + 16 * i);
-    const int see_hi = live && len >= 0 && len <= a.max_len ? max(min(len - a.Tq + t % a.Tq + 1, last), 0) : 0;
-    int all_hi = live ? see_hi : last;  // where what all of the wave's rows see ends
-    if (__ballot(all_hi != last))
+    const int see_hi = live && len >= 0 && len <= a.max_len ? max(min(len - a.Tq + t % a.Tq + 1, end), 0) : 0;
+    int all_hi = live ? see_hi : end;  // where what all of the wave's rows see ends
+    if (__ballot(all_hi != end))
 #pragma unroll
         for (int x = 1; x < 32; x <<= 1) all_hi = min(all_hi, shfl_xor(all_hi, x));
     all_hi = __builtin_amdgcn_readfirstlane(all_hi);
+    int any_hi = see_hi;  // and what any of them sees
+    if (!__ballot(any_hi == end))
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) any_hi = max(any_hi, shfl_xor(any_hi, x));
+    else
+        any_hi = end;
+    if (lane == 0) sh.seen[wave] = any_hi;
     lds_barrier();
     bool any_bad = false;
 #pragma unroll
     for (int w = 0; w < kDecWaves; ++w) any_bad |= sh.bad[w] != 0;
     any_bad = __builtin_amdgcn_readfirstlane(any_bad);
+    // behind what any row sees there may be anything, also scales that are NaN: 0 * NaN
+    int last = first;
+#pragma unroll
+    for (int w = 0; w < kDecWaves; ++w) last = max(last, sh.seen[w]);
+    last = __builtin_amdgcn_readfirstlane(last);
 
     // A tile's bytes: keys by 32 channels of a position, values by 8 channels of four.  What lies
     // behind the end or on a bad page is read at the chunk's first place, or page 0, and has the scale 0.
