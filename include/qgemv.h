@@ -619,9 +619,10 @@ int attn_prefill(int type, const void *q, int ldq, const void *k, int ldk, const
  * type out_type, which is `type`, or any if that is QG_TYPE_F32; they may be q and k
  * themselves, with the same row strides, if the types are equal.  Sums and angles: fp32,
  * but p * freq is taken in 64 bits; the error of an fp32 result is below 2^-18 times the
- * larger magnitude of its pair, and other types are rounded once.  Squares may be of any size.  Rows of
- * no sequence, or of one left out by a data error, and parts of rows between the heads and
- * the stride are not written, nor read with any effect.
+ * larger magnitude of its pair, or 2^-126 (times w, if that is larger), and other types are
+ * rounded once.  Squares may be of any size: finite heads up to the type's largest have
+ * finite norms.  Rows of no sequence, or of one left out by a data error, and parts of rows
+ * between the heads and the stride are not written, nor read with any effect.
  * Data errors: sequence b is left out (QG_DEV_BAD_LENGTH) if cu[b] < 0, cu[b+1] < cu[b],
  * cu[b+1] > n, lens[b] < its new tokens or lens[b] >= 2^30; where cu decreases, any other
  * sequence may be left out too.

@@ -171,18 +171,22 @@ __global__ __launch_bounds__(kRopeWaves *kWave) void qk_norm_rope_kernel(RopeArg
 #pragma unroll
     for (int j = 0; j < 16; ++j) sum = __builtin_fmaf(x[j], x[j], sum);
     sum = head_sum<LANES>(sum);
-    float eps = a.eps;
-    if (TIN != QG_TYPE_F16 && !(sum <= 0x1p126f)) {  // squares beyond fp32: all of it 2^64 times smaller
+    auto inverse = [](float sum, float eps) { return 1.f / __builtin_sqrtf(sum * (1.f / DH) + eps); };
+    float r;
+    // Squares beyond fp32: those of elements 2^72 times smaller, of which 256 of the largest stay inside it.  Half of the
+    // factor goes to the elements and half to r, which would be subnormal with all of it.
+    if (TIN != QG_TYPE_F16 && !(sum <= 0x1p126f)) {
         sum = 0.f;
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-            x[j] *= 0x1p-64f;
-            sum = __builtin_fmaf(x[j], x[j], sum);
+            const float y = x[j] * 0x1p-72f;
+            sum = __builtin_fmaf(y, y, sum);
+            x[j] *= 0x1p-36f;
         }
-        sum = head_sum<LANES>(sum);
-        eps *= 0x1p-128f;
+        r = inverse(head_sum<LANES>(sum), a.eps * 0x1p-144f) * 0x1p-36f;
+    } else {
+        r = inverse(sum, a.eps);
     }
-    const float r = 1.f / __builtin_sqrtf(sum * (1.f / DH) + eps);
 #pragma unroll
     for (int j = 0; j < 16; ++j) x[j] *= r;
 #pragma unroll
