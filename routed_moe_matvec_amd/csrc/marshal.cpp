@@ -5,7 +5,7 @@
 //
 //  rows, array   the address of a tensor that is on the call's device, of its type and
 //                large enough; for anything else what the binding's functions of the same
-//                arguments, which look closer and say what is wrong, return (otherwise(rows, array))
+//                arguments, which look closer and say what is wrong, return or raise (otherwise(rows, array))
 //  the calls     of qgemv.h by their own names, addresses and sizes as integers; every
 //                call of the library runs without the interpreter's lock
 #include <Python.h>
@@ -13,6 +13,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <climits>
+#include <exception>
 #include <tuple>
 #include <type_traits>
 #include <utility>
@@ -81,9 +82,17 @@ const void *find_array(PyObject *const *args, Py_ssize_t n) {
     return have < count ? nullptr : t->data_ptr();
 }
 
+// Tensors without memory of their own (those that vmap and grad wrap others in, sparse ones) throw where they
+// are asked for it, or for strides: nothing may leave a C entry so, and the function of the same arguments says it.
 template <auto FIND, PyObject **OTHER>
 PyObject *address(PyObject *, PyObject *const *args, Py_ssize_t n) {
-    if (const void *p = FIND(args, n)) return PyLong_FromVoidPtr(const_cast<void *>(p));
+    const void *p = nullptr;
+    try {
+        p = FIND(args, n);
+    } catch (const std::exception &) {
+        PyErr_Clear();
+    }
+    if (p) return PyLong_FromVoidPtr(const_cast<void *>(p));
     return PyObject_Vectorcall(*OTHER, args, n, nullptr);
 }
 
