@@ -11,12 +11,14 @@
 //
 // Operands are fp16 where a chunk's scales span no more than fp16 holds exactly, 36 binades, with
 // one power of two taken off all keys and one off all values; a weight, times 2^11, is then two
-// parts (22 bits, or 2^-36 of the row's largest), an fp32 query two (24 bits of what is
-// within 2^26 of the row's largest, else the chunk is not taken so) and an fp16 one itself.  Other
+// parts (22 bits, or 2^-36 of the row's largest), an fp32 query two and an fp16 one itself.  The second
+// part of a query is taken 2^12 times as large, or fp16's least step would cut it, and its products are summed
+// first: an element is off by 2^-23 of itself at most if it is within 2^26 of the row's largest; where one is not, the chunk
+// is not taken so.  (The same sum for both parts lost bits from 2^17 on, at 134 us in place of 138 for the case below.)  Other
 // chunks, and the keys of bf16 queries, take bf16, which holds every value exactly, and
 // three parts for 24 bits: fp32, fp16, bf16 queries need 4, 3, 3 products so, and 6, 5, 4 there
 // (fp32 and fp16 queries are read and split again at every tile).  48 sequences of 8 rows a head of
-// fp32 queries over 40001 positions, 63 GFLOP, 127 with the parts, take 125 to 146 us by the run: the
+// fp32 queries over 40001 positions, 63 GFLOP, 127 with the parts, take 125 to 150 us by the run: the
 // matrix cores are busy 52% of the cycles, the vector units 47% (without the issue of matrix
 // instructions), both at once 19%, at 2.1 GHz, and neither another order of the instructions nor wave
 // priorities changed that.  Few positions are bound by latency.  32 sequences of 4 rows over 6001: 4.3
@@ -274,7 +276,7 @@ __device__ __forceinline__ void attn_prefix_group(const DecodeArgs &a, PfxShared
         const float most = half_max(__builtin_bit_cast(float, most_q));
         const float least = least_q == ~0u ? INFINITY : __builtin_bit_cast(float, least_q + 1);
         if (most > 0.f) qexp = __builtin_amdgcn_frexp_expf(most) - 15;
-        // two parts hold 24 bits of what is within 2^26 of the row's largest
+        // the first part of what is within 2^26 of the row's largest is a normal number: two parts are off by 2^-23 of it
         const bool wide = __ballot(least * 0x1p26f < most || qexp < -60 || qexp > 60) != 0;
         if (lane == 0) sh.wide[wave] = wide;
     }
@@ -305,6 +307,7 @@ __device__ __forceinline__ void attn_prefix_group(const DecodeArgs &a, PfxShared
     const float scale = __builtin_ldexpf(a.scale, qexp - dk);  // of a row's scores as they are computed
 
     u32x4 qf[QF][KC];
+    constexpr float kRest = 0x1p12f;  // on the second part of a query: at most 2^3 without
     if constexpr (TYPE == QG_TYPE_F32) {
         const float factor = a.qsign * __builtin_ldexpf(1.f, -qexp);
 #pragma unroll
@@ -315,7 +318,7 @@ __device__ __forceinline__ void attn_prefix_group(const DecodeArgs &a, PfxShared
                 const f16x2 hi = __builtin_convertvector((f32x2{x0, x1}), f16x2);
                 const f32x2 rest = {__builtin_fmaf((float)hi[0], -1.f, x0), __builtin_fmaf((float)hi[1], -1.f, x1)};
                 qf[0][i][e] = __builtin_bit_cast(uint32_t, hi);
-                qf[1][i][e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest, f16x2));
+                qf[1][i][e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest * kRest, f16x2));
             }
     } else {
         const uint32_t flip = a.qsign < 0.f ? 0x80008000u : 0u, keep = a.qsign == 0.f ? 0u : ~0u;
@@ -342,20 +345,31 @@ __device__ __forceinline__ void attn_prefix_group(const DecodeArgs &a, PfxShared
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int x = 0; x < 16; ++x) s[n][x] = 0.f;
+        auto key = [&](int n, int i) {
+            const int r = r0 + 32 * n + c;
+            return *(const u32x4 *)(sk + r * DH * 2 + 16 * L::k_piece(r, 2 * i + hf));
+        };
+        if constexpr (F && QF == 2) {  // the second parts first, then what was on them taken off
+#pragma unroll
+            for (int i = 0; i < KC; ++i)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) s[n] = PfxOps<KF>::mfma(key(n, i), qf[1][i], s[n]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) s[n] *= 1 / kRest;
+            asm volatile("" ::: "memory");  // or the keys stay in registers for the products below, which spill
+        }
 #pragma unroll
         for (int i = 0; i < KC; ++i) {
             bf16x8 slow[QS];  // rare: read and split again at each tile, no registers kept
             if constexpr (!F && QS > 1) split8<QS>(load8(qp + 16 * i), a.qsign, slow);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const int r = r0 + 32 * n + c;
-                const u32x4 kf = *(const u32x4 *)(sk + r * DH * 2 + 16 * L::k_piece(r, 2 * i + hf));
+                const u32x4 kf = key(n, i);
                 if constexpr (!F && QS > 1) {
 #pragma unroll
                     for (int p = 0; p < QS; ++p) s[n] = PfxOps<false>::mfma(kf, __builtin_bit_cast(u32x4, slow[p]), s[n]);
                 } else {
-#pragma unroll
-                    for (int p = 0; p < QF; ++p) s[n] = PfxOps<KF>::mfma(kf, qf[p][i], s[n]);
+                    s[n] = PfxOps<KF>::mfma(kf, qf[0][i], s[n]);
                 }
             }
         }
