@@ -670,9 +670,9 @@ int attn_prefill_sinks(int type, const void *q, int ldq, const void *k, int ldk,
  * the prefix; a sequence may also end inside it (lens[b] = 0 for an unused row of the batch).
  * prefix = 0 (prefix_pages may be NULL) is attn_decode_kv4.  Results agree with
  * attn_decode_kv4's over a table whose blocks name the same keys and values to rounding; one
- * sequence's may depend on the batch by rounding.  The error is as there, but that over
- * the prefix an element of an fp32 query may be off by 2^-23 of itself, and weights below
- * 2^-11 of a row's largest by 2^-36 of that.
+ * sequence's may depend on the batch by rounding, but not on max_len.  The error is as
+ * there, but that over the prefix an element of an fp32 query may be off by 2^-23 of
+ * itself, and weights below 2^-11 of a row's largest by 2^-36 of that.
  * ws: attn_decode_prefix_workspace_bytes(...) bytes.
  * Data errors: as attn_decode_kv4; a bad page of the prefix is left out for all.
  * Errors: as attn_decode_kv4; QG_ERR_SHAPE unless 0 <= prefix <= max_len, and where its

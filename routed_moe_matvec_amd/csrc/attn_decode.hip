@@ -122,7 +122,7 @@ static int launch_decode_dh(const DecodeArgs &a, hipStream_t stream) {
     }
     int rc;
     if constexpr (DH <= 128)
-        if (a.wide) return a.prefix ? launch_decode_mode<TYPE, DH, FUSED, 8>(a, stream) : launch_decode_mode<TYPE, DH, SINKS, 8>(a, stream);
+        if (a.wide) return launch_decode_mode<TYPE, DH, SINKS, 8>(a, stream);
     if (a.prefix)
         rc = launch_decode_mode<TYPE, DH, FUSED>(a, stream);
     else
@@ -148,26 +148,27 @@ struct DecodeChunks {
     bool wide;  // one chunk, of eight waves
     int all;    // chunks of the prefix and a sequence
 };
-// With two ranges of up to 1280 positions of 128 channels a sequence is one chunk, which eight waves
+// With sinks and up to 1280 positions of 128 channels a sequence is one chunk, which eight waves
 // share: no join.  us with that, and with chunks of four waves: 1024 positions and 4 sinks of 1, 16, 32,
 // 64 sequences with 8 key heads 9.9, 10.4, 11.5, 18.5 and 8.8, 11.6, 16.7, 26; 2048 15, 16, 17.5,
 // 29 and 10.5, 14.6, 21.9, 35; 500 7.8, 7.9, 8.3, 12.3 and 8.7, 8.8, 9.1, 12.2.  A rule of the call's
-// window and sinks: a sequence's result does not depend on max_len.
+// window and sinks: a sequence's result does not depend on max_len.  A walk over a short shared prefix knows no other
+// bound than that, and so takes four waves at any length (us with four, and with eight in one chunk: 4 sequences of 301
+// to 431 positions 8.6, 7.9, of 1100 9.3, 10.5, 16 of 1100 12.1, 11.0).
 static DecodeChunks decode_chunks(int B, int Tq, int G, int Hkv, int Dh, int max_len, int window, int sinks, int prefix) {
     DecodeChunks n{{0, 0, 0}, dec_split(G * Tq, Dh), false, 0};
-    long long most = max_len, two = 1LL << 40;
+    long long most = max_len, held = 1LL << 40;
     if (prefix) n.prefix = prefix_split(B, (long long)B * Tq * G, Hkv, Dh, prefix);
     if (n.prefix.chunks) {
         n.own.least = 11 + 7 - n.own.dh_log2;
         most = max_len > prefix ? max_len - (prefix & ~15) : 0;
     } else if (prefix) {
-        most = two = max_len + 16LL;
+        most = max_len + 16LL;
     } else if (window) {
-        const long long held = (long long)window + Tq - 1 + 15 + (sinks + 15LL) / 16 * 16;
-        if (sinks) two = held;
+        held = (long long)window + Tq - 1 + 15 + (sinks + 15LL) / 16 * 16;
         if (held < most) most = held;
     }
-    if (two * Dh <= 1280 * 128 && Dh <= 128) {
+    if (sinks && held * Dh <= 1280 * 128 && Dh <= 128) {
         n.wide = true;
         n.own.least = 13;
     }
