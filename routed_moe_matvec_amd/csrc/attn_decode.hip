@@ -108,6 +108,25 @@ static int launch_decode_mode(const DecodeArgs &a, hipStream_t stream) {
     return hipGetLastError() == hipSuccess ? QG_OK : QG_ERR_LAUNCH;
 }
 
+// One chunk a sequence, of eight waves.  A launch holds fewer than 2^32 threads, so half of the workgroups that a
+// call may need: the sequences then go in two launches.
+template <int TYPE, int DH>
+static int launch_decode_wide(const DecodeArgs &a, hipStream_t stream) {
+    const int B = a.c.B, each = (int)(kMaxGroups / 2 / ((long long)a.c.Hkv * ((a.G * a.Tq + 15) / 16)));
+    for (int b = 0; b < B; b += each) {
+        DecodeArgs part = a;
+        const size_t rows = (size_t)b * a.Tq;
+        part.c.B = B - b < each ? B - b : each;
+        part.c.lens += b;
+        part.c.pages += (size_t)b * a.c.max_pages;
+        part.q = (const uint8_t *)a.q + rows * a.ldq * elem_bytes(TYPE);
+        part.y += rows * a.H * DH;
+        const int rc = launch_decode_mode<TYPE, DH, SINKS, 8>(part, stream);
+        if (rc != QG_OK) return rc;
+    }
+    return QG_OK;
+}
+
 template <int DH, int MODE>
 static int launch_join(const DecodeArgs &a, hipStream_t stream) {
     hipLaunchKernelGGL((attn_decode_join_kernel<DH, MODE>), dim3(a.H * a.Tq, a.c.B), dim3(256), 0, stream, a);
@@ -122,7 +141,7 @@ static int launch_decode_dh(const DecodeArgs &a, hipStream_t stream) {
     }
     int rc;
     if constexpr (DH <= 128)
-        if (a.wide) return launch_decode_mode<TYPE, DH, SINKS, 8>(a, stream);
+        if (a.wide) return launch_decode_wide<TYPE, DH>(a, stream);
     if (a.prefix)
         rc = launch_decode_mode<TYPE, DH, FUSED>(a, stream);
     else
