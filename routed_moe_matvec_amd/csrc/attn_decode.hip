@@ -23,9 +23,10 @@
 // shared prefixes (FUSED): places are counted over two ranges of positions, each from a
 // multiple of 16, and a tile lies in one of them.  32 sequences of up to 20000 positions with a window
 // of 1024 and 4 sinks, 32 heads of 128: 10.9 us, 35 MB; 24 of up to 60000 with a window of
-// 8192 and 100 sinks, 3 tokens, 16 heads of 64: 58 us, 196 MB, bound by vector
-// instructions (76% of the cycles, without the issue of matrix instructions: every cached value
-// is converted for 3 rows only).
+// 8192 and 100 sinks, 3 tokens, 16 heads of 64: 55 to 60 us, 196 MB, bound by vector
+// instructions (75% of the cycles, without the issue of matrix instructions).  Of a step's about 80 are the softmax and the
+// weights' parts, on 16 columns of which 3 are rows (its 8 exponentials take four times as long as others), and about 65
+// the conversion and pairing of keys and values.
 #include <type_traits>
 
 #include "attn_decode_device.h"

@@ -18,8 +18,8 @@
 // chunks, and the keys of bf16 queries, take bf16, which holds every value exactly, and
 // three parts for 24 bits: fp32, fp16, bf16 queries need 4, 3, 3 products so, and 6, 5, 4 there
 // (fp32 and fp16 queries are read and split again at every tile).  48 sequences of 8 rows a head of
-// fp32 queries over 40001 positions, 63 GFLOP, 127 with the parts, take 125 to 150 us by the run: the
-// matrix cores are busy 52% of the cycles, the vector units 47% (without the issue of matrix
+// fp32 queries over 40001 positions, 63 GFLOP, 127 with the parts, take 130 to 150 us by the run: the
+// matrix cores are busy 51% of the cycles, the vector units 49% (without the issue of matrix
 // instructions), both at once 19%, at 2.1 GHz, and neither another order of the instructions nor wave
 // priorities changed that.  Few positions are bound by latency.  32 sequences of 4 rows over 6001: 4.3
 // us to the first tile, 2.8 for it, 1.7 for each further one of 128, 2 for the sums.
@@ -581,7 +581,7 @@ static int launch_prefix(const DecodeArgs &a, int Dh, hipStream_t stream) {
 // sequences of 8 rows a head over 40001: 128 rows in 21 chunks 128, in 11 168, 64 rows 145, 32
 // rows 173; 32 of 4 rows over 6001: 128 rows in 32 chunks 27, 64 in 16 26, 32 in 8 24, in 16 31.
 // Each sequence by itself (no chunks) takes about 22 for 10^6 times 16 rows' positions, and
-// 3 less to begin with: 4 sequences over 300 8.4 and 13.9, 2 over 30000 20 and 28, 48 of 16 rows
+// 3 less to begin with: 4 sequences over 300 8.6 and 13.9, 2 over 30000 20 and 28, 48 of 16 rows
 // over 1500 28 and 34, 16 of 4 rows over 4000 22 and 18, 8 of 2 over 16000 27 and 18.
 PrefixSplit prefix_split(int B, long long rows, int Hkv, int Dh, int prefix) {
     PrefixSplit best{0, 0, 0};
