@@ -174,7 +174,8 @@ struct DecodeChunks {
 // 29 and 10.5, 14.6, 21.9, 35; 500 7.8, 7.9, 8.3, 12.3 and 8.7, 8.8, 9.1, 12.2.  A rule of the call's
 // window and sinks: a sequence's result does not depend on max_len.  A walk over a short shared prefix knows no other
 // bound than that, and so takes four waves at any length (us with four, and with eight in one chunk: 4 sequences of 301
-// to 431 positions 8.6, 7.9, of 1100 9.3, 10.5, 16 of 1100 12.1, 11.0).
+// to 431 positions 8.6, 7.9, of 1100 9.3, 10.5, 16 of 1100 12.1, 11.0, 64 channels: 4 of 2000 10.3, 13.0, 16 of 1300
+// 15.2, 10.0).
 static DecodeChunks decode_chunks(int B, int Tq, int G, int Hkv, int Dh, int max_len, int window, int sinks, int prefix) {
     DecodeChunks n{{0, 0, 0}, dec_split(G * Tq, Dh), false, 0};
     long long most = max_len, held = 1LL << 40;
